@@ -53,15 +53,39 @@ typedef enum {
     MOE_F32 = 0,     /* IEEE binary32                                          */
     MOE_BF16 = 1,    /* bfloat16                                               */
     MOE_FP8_E4M3 = 2, /* OCP OFP8 E4M3 (bias 7, max 448, no inf) + float32 scale */
-    MOE_W4A16 = 3     /* weights: 4-bit codes with a float32 scale per 128 k of a row;
+    MOE_W4A16 = 3,    /* weights: 4-bit codes with a float32 scale per 128 k of a row;
                          activations and outputs bfloat16 (see moe_grouped_gemm) */
+    MOE_FP8_BLOCK = 4 /* weights: e4m3 codes with a float32 scale per 128 x 128 block;
+                         token rows e4m3 with a scale per 128 k (moe_quant_block);
+                         layer inputs and outputs bfloat16 (see moe_grouped_gemm) */
 } moe_dtype;
 
 typedef enum {
     MOE_GEMM_GATE_UP_SILU = 0, /* act[p] = silu(W1[e][0:I] x) * (W1[e][I:2I] x) */
     MOE_GEMM_DOWN = 1,         /* y[p]   = W2[e] act[p]                         */
-    MOE_GEMM_DOWN_E4M3_ACT = 2 /* as DOWN, act given as e4m3 codes (moe_quant_act) */
+    MOE_GEMM_DOWN_E4M3_ACT = 2, /* as DOWN, act given as e4m3 codes (moe_quant_act) */
+    MOE_GEMM_GATE_UP_SILU_E4M3 = 3 /* MOE_FP8_BLOCK only: as GATE_UP_SILU, act as e4m3
+                                      codes with a scale per 128 columns of a row */
 } moe_gemm_kind;
+
+/* Scores a router's logits turn into (moe_routing). */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0, /* s_e = exp(l_e) / sum over all E experts */
+    MOE_SCORE_SIGMOID = 1  /* s_e = 1 / (1 + exp(-l_e))               */
+} moe_score;
+
+/* How a grouped router chooses and weighs its experts (moe_route_grouped). */
+typedef struct {
+    moe_score score;
+    const float* bias;    /* device float32 [E] added to the scores for the choice only
+                             (load balance), 4-byte aligned, or NULL */
+    int32_t n_groups;     /* groups of E / n_groups consecutive experts; 1: no groups */
+    int32_t topk_groups;  /* groups a token may choose from, 1..n_groups */
+    int32_t group_top;    /* a group's score: the best choice (1) or the sum of the two
+                             best choices (2) among its experts */
+    int32_t renormalize;  /* != 0: weights are divided by their sum over the chosen */
+    float scale;          /* factor on the weights, finite */
+} moe_routing;
 
 /* The index system produced by moe_align (all device pointers, int32):
  *  sorted_ids[cap]        pair ids p = t*topk + j grouped by expert, stable in p;
@@ -114,6 +138,35 @@ moe_status moe_router_logits(moe_dtype x_dtype, const void* x, const float* x_sc
 moe_status moe_route(const float* logits, int32_t M, int32_t E, int32_t topk, int32_t renormalize,
                      int32_t* topk_ids, float* topk_weights, void* stream);
 
+/* Top-k routing with a score function, a balance bias and expert groups (the
+ * router of fine-grained layers; section 2 with the choice limited to a few
+ * groups of experts).  Per token, with scores s (moe_score):
+ *  1. choice c_e = s_e + bias_e, compared in float64;
+ *  2. with topk_groups < n_groups, a group's score is its best c, or the sum
+ *     of its two best (group_top), and the topk_groups best groups stay in;
+ *  3. the topk best c among the groups left are chosen, slot j the j-th
+ *     best; equal choices go to the lower expert (group) index.  Without a
+ *     bias experts are ranked by their logits, which both scores rise with
+ *     (so logits whose scores round alike keep their order);
+ *  4. w_j = s_j (without the bias), / sum of the chosen s if renormalize,
+ *     times scale, float32.
+ * Ids are those of exact arithmetic to float64: float32 decides where its
+ * error cannot change the choice, float64 decides the rest.
+ * A logit of -inf has score 0; NaN logits count as -inf, and a choice or
+ * group score that is NaN ranks with -inf.  +inf logits share a softmax's
+ * mass evenly.  Softmax of a row with nothing above -inf: scores 0.  Weights
+ * whose sum is 0 stay 0.
+ *  logits_dtype  MOE_F32 or MOE_BF16
+ *  logits        device [M][E]
+ *  topk_ids, topk_weights  device int32 / float32 [M][topk]
+ * Errors: NULL -> MOE_ERR_NULL; M<0, E<1, topk<1, topk>E, n_groups not a
+ * divisor of E, topk_groups outside [1, n_groups], group_top not 1 or 2 or
+ * larger than a group, topk above the experts of topk_groups groups, scale
+ * not finite -> MOE_ERR_SHAPE; E>256, topk>16, n_groups>64, unknown score or
+ * dtype -> MOE_ERR_UNSUPPORTED. */
+moe_status moe_route_grouped(moe_dtype logits_dtype, const void* logits, const moe_routing* routing, int32_t M,
+                             int32_t E, int32_t topk, int32_t* topk_ids, float* topk_weights, void* stream);
+
 /* Rows of sorted_ids needed by moe_align: the smallest multiple of block_m
  * that is >= P + min(E, P) * (block_m - 1), P = M*topk.  Pure host function;
  * returns -1 for invalid arguments. */
@@ -158,12 +211,27 @@ moe_status moe_align(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E
  *         amax, and a_scale -> that amax.  Same codes, same scales, same
  *         products as MOE_GEMM_DOWN; the rows are read at one byte per value
  *         (what the tile kernels want when many rows share an expert).
- *  a_scale, w_scale, c_amax must be NULL unless dtype is MOE_FP8_E4M3.
+ *         MOE_FP8_BLOCK (block-scaled e4m3): w = e4m3 [E][N][K] with w_scale
+ *         float32 [E][N/128][K/128], and
+ *           c[p][n] = sum_b sa[p][b] * sw[e][n/128][b] * sum_{k in block b} a[p][k] * w[n][k],
+ *         the products of a block of 128 k summed on the MFMA, the blocks in
+ *         float32.  GATE_UP_SILU: a = e4m3 codes [M][K] with a_scale [M][K/128]
+ *         (moe_quant_block), c = act float32 [P][I].  GATE_UP_SILU_E4M3: the
+ *         same, but c = e4m3 codes [P][I] and c_amax receives their scales
+ *         [P][I/128], quantised from the float32 act as moe_quant_block does.
+ *         DOWN: a = act float32 [P][K], quantised on load the same way
+ *         (a_scale NULL), c = y bfloat16.  DOWN_E4M3_ACT: a = codes [P][K],
+ *         a_scale [P][K/128], c = y bfloat16.  The two kinds over float32 act
+ *         stream the weights once per 16 rows of an expert (small batches);
+ *         the two E4M3 kinds are the tiled ones and take block_m 32, 64 or
+ *         128 (moe_block_m), else MOE_ERR_UNSUPPORTED.
+ *  a_scale, w_scale, c_amax must be NULL unless the dtype above names them.
  *  al, block_m: the output of moe_align for the same topk_ids and block_m.
  *  Rows of a expert's run are read through al->sorted_ids; only the first
  *  expert_counts[e] rows of each run are written to c.
  * Errors as for the other calls; K and N must be multiples of 128 (K of 256
- * for MOE_FP8_E4M3). */
+ * for MOE_FP8_E4M3; GATE_UP: N of 256).  MOE_FP8_BLOCK: one expert's codes
+ * (N K bytes) of 4 GiB or more -> MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, const float* a_scale,
                             const void* w, const float* w_scale, const moe_align_bufs* al, int32_t M,
                             int32_t topk, int32_t E, int32_t N, int32_t K, int32_t block_m, void* c,
@@ -180,6 +248,23 @@ moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, 
  * n must be a multiple of 16 (MOE_ERR_SHAPE otherwise); n = 0 is a no-op. */
 moe_status moe_quant_act(const void* act, const float* amax, int64_t n, void* act_q, void* stream);
 
+/* Block-scaled e4m3 quantisation: one float32 scale for every block of
+ * block_rows x 128 values, block_rows 1 (token rows, the intermediate) or 128
+ * (weights; the last block of rows may be short).  With amax the largest
+ * magnitude of the block, s = max(amax / 448, 2^-126) and code = e4m3 of x / s
+ * (IEEE float32 quotients, round to nearest even, at most +-448), so x is
+ * about code * s.  A block of zeros has codes 0; one with an infinity or a
+ * NaN has scale NaN and every code NaN (0x7f).
+ *  x_dtype  MOE_F32 or MOE_BF16
+ *  x        device [rows][K]
+ *  q        device uint8 [rows][K], e4m3 codes
+ *  scale    device float32 [ceil(rows / block_rows)][K/128]
+ * Errors: NULL -> MOE_ERR_NULL; rows<0, K<1, K not a multiple of 128 ->
+ * MOE_ERR_SHAPE; other dtypes or block_rows -> MOE_ERR_UNSUPPORTED.
+ * rows = 0 is a no-op. */
+moe_status moe_quant_block(moe_dtype x_dtype, const void* x, int32_t rows, int32_t K, int32_t block_rows, void* q,
+                           float* scale, void* stream);
+
 /* Weighted combine back into token order (section 3.1 step 4):
  *  out[t][h] = sum_{j=0..topk-1} topk_weights[t][j] * y[t*topk+j][h], j
  *  ascending, float32 accumulation.
@@ -187,6 +272,12 @@ moe_status moe_quant_act(const void* act, const float* amax, int64_t n, void* ac
  *  y device [M*topk][H]; topk_weights device [M][topk]; out device [M][H]. */
 moe_status moe_combine(moe_dtype y_dtype, const void* y, const float* topk_weights, int32_t M,
                        int32_t topk, int32_t H, moe_dtype out_dtype, void* out, void* stream);
+
+/* Rows per tile (block_m) fused_moe aligns a batch to: a good choice for
+ * moe_align before moe_grouped_gemm.  MOE_FP8_BLOCK: 32, 64 or 128, whichever
+ * the E4M3 kinds run fastest on.  Pure host function; 0 for invalid
+ * arguments. */
+int32_t moe_block_m(moe_dtype dtype, int32_t M, int32_t E, int32_t topk);
 
 /* Bytes of device workspace fused_moe needs for these sizes (0 for M=0). */
 size_t fused_moe_workspace_size(moe_dtype dtype, int32_t M, int32_t E, int32_t topk, int32_t H,
@@ -199,13 +290,16 @@ size_t fused_moe_workspace_size(moe_dtype dtype, int32_t M, int32_t E, int32_t t
  * launch runs; topk_ids_out / topk_weights_out are then written by the
  * GATE_UP launch (e4m3: the intermediate's amax goes from the GATE_UP launch
  * to the DOWN launch as partial maxima in the workspace, the same value).
- *  x              device [M][H]: float32, bfloat16 (also for MOE_W4A16) or e4m3
- *                 (x_scale -> float32)
+ *  x              device [M][H]: float32, bfloat16 (also for MOE_W4A16 and
+ *                 MOE_FP8_BLOCK, which quantises it as moe_quant_block does)
+ *                 or e4m3 (x_scale -> float32)
  *  router_logits  device float32 [M][E]
  *  w1, w2         device [E][2I][H] and [E][H][I] in dtype (fp8: w1_scale,
  *                 w2_scale device float32 [E]; MOE_W4A16: packed codes
  *                 [E][2I][H/2] and [E][H][I/2], w1_scale [E][H/128][2I],
- *                 w2_scale [E][I/128][H], as for moe_grouped_gemm)
+ *                 w2_scale [E][I/128][H]; MOE_FP8_BLOCK: w1_scale
+ *                 [E][2I/128][H/128], w2_scale [E][H/128][I/128]; as for
+ *                 moe_grouped_gemm)
  *  out            device [M][H]: float32 for MOE_F32, bfloat16 otherwise
  *  topk_ids_out, topk_weights_out  optional device [M][topk] copies of the
  *                 routing result (NULL to skip)
@@ -222,6 +316,16 @@ moe_status fused_moe(moe_dtype dtype, const void* x, const float* x_scale, const
                      int32_t M, int32_t E, int32_t topk, int32_t H, int32_t I, int32_t renormalize,
                      void* out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/* fused_moe with a grouped router: routes router_logits (float32 [M][E]) as
+ * moe_route_grouped does, then runs the same layer, for every dtype.
+ * Workspace, the other arguments and errors as for fused_moe
+ * (fused_moe_workspace_size gives the workspace) and moe_route_grouped. */
+moe_status fused_moe_grouped(moe_dtype dtype, const void* x, const float* x_scale, const float* router_logits,
+                             const moe_routing* routing, const void* w1, const float* w1_scale, const void* w2,
+                             const float* w2_scale, int32_t M, int32_t E, int32_t topk, int32_t H, int32_t I,
+                             void* out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* fused_moe from the hidden states: the router scores are computed on the
  * GPU first (router_w device float32 [E][H]; router_logits is then an OUTPUT,
@@ -281,8 +385,10 @@ size_t fused_moe_noalloc_scratch_bytes(void);
 typedef struct {
     const void* w1;        /* [n][2I][H] (MOE_W4A16: packed codes [n][2I][H/2]) */
     const void* w2;        /* [n][H][I]  (MOE_W4A16: [n][H][I/2])               */
-    const float* w1_scale; /* fp8: [n]; MOE_W4A16: [n][H/128][2I]; else NULL    */
-    const float* w2_scale; /* fp8: [n]; MOE_W4A16: [n][I/128][H];  else NULL    */
+    const float* w1_scale; /* fp8: [n]; MOE_W4A16: [n][H/128][2I]; MOE_FP8_BLOCK:
+                              [n][2I/128][H/128]; else NULL                     */
+    const float* w2_scale; /* fp8: [n]; MOE_W4A16: [n][I/128][H]; MOE_FP8_BLOCK:
+                              [n][H/128][I/128]; else NULL                      */
 } moe_expert_weights;
 
 /* Opaque cache state (host bookkeeping and HIP events). */

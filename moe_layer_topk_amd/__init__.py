@@ -9,10 +9,15 @@ Steps of the layer (FusedMoE vs MegaMoE post, sections 2 and 3.1):
 moe_route -> moe_align -> moe_grouped_gemm (gate/up + SiLU-and-mul, then
 down) -> moe_combine, or all of them in one call with fused_moe.  For e4m3
 weights the intermediate is float32 and the down call quantises it on load;
-moe_quant_act gives the same codes as a tensor.
+moe_quant_act gives the same codes as a tensor.  Block-scaled e4m3 (weights
+float8_e4m3fn with 3-D float32 scales, one per 128 x 128 block): moe_quant_block
+-> moe_grouped_gemm with the E4M3 kinds, or the fused layers from bfloat16
+hidden states.  moe_route_grouped / fused_moe_grouped route with a Routing
+(softmax or sigmoid scores, balance bias, expert groups).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -23,13 +28,18 @@ from ._lib import (  # noqa: F401
     MOE_W4A16,
     MOE_BF16,
     MOE_F32,
+    MOE_FP8_BLOCK,
     MOE_FP8_E4M3,
     MOE_GEMM_DOWN,
     MOE_GEMM_DOWN_E4M3_ACT,
     MOE_GEMM_GATE_UP_SILU,
+    MOE_GEMM_GATE_UP_SILU_E4M3,
+    MOE_SCORE_SIGMOID,
+    MOE_SCORE_SOFTMAX,
     AlignBufs,
     ExpertWeights,
     MoeError,
+    RoutingArgs,
     check,
     lib,
 )
@@ -37,7 +47,7 @@ from ._lib import (  # noqa: F401
 # weight storage -> layer dtype (uint8 weights are packed int4 codes, W4A16)
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_FP8_E4M3, torch.uint8: MOE_W4A16}
 _INTER = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_FP8_E4M3: torch.bfloat16,
-          MOE_W4A16: torch.bfloat16}  # y and out
+          MOE_W4A16: torch.bfloat16, MOE_FP8_BLOCK: torch.bfloat16}  # y and out
 _ACT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_FP8_E4M3: torch.float32,
         MOE_W4A16: torch.bfloat16}  # the intermediate
 
@@ -57,6 +67,86 @@ def moe_dtype(t: torch.Tensor) -> int:
         return _DTYPES[t.dtype]
     except KeyError:
         raise ValueError(f"unsupported dtype {t.dtype}") from None
+
+
+def _layer_dtype(w: torch.Tensor, w_scale) -> int:
+    """The layer dtype of expert weights: e4m3 with 3-D scales is block-scaled."""
+    if w.dtype == torch.float8_e4m3fn and w_scale is not None and w_scale.dim() == 3:
+        return MOE_FP8_BLOCK
+    return moe_dtype(w)
+
+
+def _on(t: torch.Tensor):
+    """The context in which t's device is the current one (the library launches on it)."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _need(name: str, t, dtypes, shape, device) -> None:
+    """A contiguous tensor of one of the dtypes, of this shape, on this device."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is missing")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+_F32, _F8 = (torch.float32,), (torch.float8_e4m3fn,)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+class Routing:
+    """How a grouped router scores and chooses its experts (moe_routing in
+    include/moe.h): score "softmax" or "sigmoid", a float32 bias [E] for the
+    choice only (or None), n_groups groups of consecutive experts of which a
+    token may use topk_groups, a group's score the best (group_top 1) or the
+    sum of the two best (2) choices in it, renormalised weights, a factor."""
+
+    _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+    def __init__(self, score: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                 renormalize: bool = True, scale: float = 1.0):
+        if score not in self._SCORES:
+            raise ValueError(f"score is one of {sorted(self._SCORES)}, got {score!r}")
+        if bias is not None:
+            if not bias.is_cuda:
+                raise ValueError("moe_layer_topk_amd computes on the GPU only; got a CPU bias")
+            _need("bias", bias, _F32, (bias.numel(),), bias.device)
+        self.bias = bias  # kept alive: the calls read it
+        self.args = RoutingArgs(self._SCORES[score], None if bias is None else bias.data_ptr(), n_groups, topk_groups,
+                                group_top, int(renormalize), scale)
+        self._ref = ctypes.byref(self.args)
+
+    def _check(self, E: int, device) -> None:
+        if self.bias is not None and (self.bias.numel() != E or self.bias.device != device):
+            raise ValueError(f"the bias has {self.bias.numel()} entries on {self.bias.device}, "
+                             f"the logits {E} experts on {device}")
+
+
+def moe_route_grouped(logits: torch.Tensor, topk: int, routing: Routing, topk_ids=None, topk_weights=None):
+    """Top-k ids (int32 [M,k]) and weights (float32 [M,k]) of a grouped router
+    from float32 or bfloat16 logits [M,E]."""
+    M, E = logits.shape
+    dev = logits.device
+    stream = _stream(logits)
+    _need("logits", logits, (torch.float32, torch.bfloat16), (M, E), dev)
+    routing._check(E, dev)
+    if topk_ids is None:
+        topk_ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+    if topk_weights is None:
+        topk_weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+    _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
+    _need("topk_weights", topk_weights, _F32, (M, topk), dev)
+    with _on(logits):
+        check(lib().moe_route_grouped(_DTYPES[logits.dtype], _p(logits), routing._ref, M, E, topk, _p(topk_ids),
+                                      _p(topk_weights), stream), "moe_route_grouped")
+    return topk_ids, topk_weights
 
 
 def moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True, topk_ids=None, topk_weights=None):
@@ -103,7 +193,9 @@ def moe_grouped_gemm(kind: int, a: torch.Tensor, w: torch.Tensor, al: dict, M: i
                      a_scale=None, w_scale=None, c=None, c_amax=None):
     """GATE_UP: act[P, N/2] = silu(gate) * up;  DOWN: y[P, N].  Returns (c, c_amax)."""
     E, N, K = w.shape
-    dt = moe_dtype(w)
+    dt = _layer_dtype(w, w_scale)
+    if dt == MOE_FP8_BLOCK:
+        return _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_amax)
     if dt == MOE_W4A16:
         K *= 2  # two 4-bit codes per byte
     P = M * topk
@@ -120,6 +212,59 @@ def moe_grouped_gemm(kind: int, a: torch.Tensor, w: torch.Tensor, al: dict, M: i
     check(lib().moe_grouped_gemm(kind, dt, _p(a), _p(a_scale), _p(w), _p(w_scale), ctypes.byref(bufs), M, topk,
                                  E, N, K, al["block_m"], _p(c), _p(c_amax), _stream(w)), "moe_grouped_gemm")
     return c, c_amax
+
+
+def _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_scale):
+    """moe_grouped_gemm on block-scaled e4m3 weights; returns (c, scales of c or None)."""
+    E, N, K = w.shape
+    P, dev = M * topk, w.device
+    stream = _stream(w)
+    gate = kind in (MOE_GEMM_GATE_UP_SILU, MOE_GEMM_GATE_UP_SILU_E4M3)
+    codes = kind in (MOE_GEMM_GATE_UP_SILU_E4M3, MOE_GEMM_DOWN_E4M3_ACT)
+    rows, cols = (M, N // 2) if gate else (P, N)
+    _need("w", w, _F8, (E, N, K), dev)
+    _need("w_scale", w_scale, _F32, (E, N // 128, K // 128), dev)
+    if kind == MOE_GEMM_DOWN:
+        _need("a", a, _F32, (rows, K), dev)
+    else:
+        _need("a", a, _CODES, (rows, K), dev)
+        _need("a_scale", a_scale, _F32, (rows, K // 128), dev)
+    cdt = torch.bfloat16 if not gate else torch.float8_e4m3fn if codes else torch.float32
+    if c is None:
+        c = torch.empty((P, cols), dtype=cdt, device=dev)
+    _need("c", c, _CODES if gate and codes else (cdt,), (P, cols), dev)
+    if kind == MOE_GEMM_GATE_UP_SILU_E4M3:
+        if c_scale is None:
+            c_scale = torch.empty((P, cols // 128), dtype=torch.float32, device=dev)
+        _need("c_amax (the scales of c)", c_scale, _F32, (P, cols // 128), dev)
+    bufs = align_struct(al)
+    with _on(w):
+        check(lib().moe_grouped_gemm(kind, MOE_FP8_BLOCK, _p(a), _p(a_scale), _p(w), _p(w_scale), ctypes.byref(bufs),
+                                     M, topk, E, N, K, al["block_m"], _p(c), _p(c_scale), stream), "moe_grouped_gemm")
+    return c, c_scale
+
+
+def moe_quant_block(x: torch.Tensor, block_rows: int = 1, q=None, scale=None):
+    """Block-scaled e4m3 of x [rows, K] (float32 or bfloat16): (codes float8_e4m3fn
+    [rows, K], float32 scales [ceil(rows / block_rows), K / 128]); block_rows 1
+    for token rows, 128 for weights."""
+    rows, K = x.shape
+    dev = x.device
+    stream = _stream(x)
+    _need("x", x, (torch.float32, torch.bfloat16), (rows, K), dev)
+    if block_rows < 1:
+        raise ValueError("block_rows is 1 or 128")
+    shape = (-(-rows // block_rows), K // 128)
+    if q is None:
+        q = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    _need("q", q, _CODES, (rows, K), dev)
+    _need("scale", scale, _F32, shape, dev)
+    with _on(x):
+        check(lib().moe_quant_block(_DTYPES[x.dtype], _p(x), rows, K, block_rows, _p(q), _p(scale), stream),
+              "moe_quant_block")
+    return q, scale
 
 
 def moe_quant_act(act: torch.Tensor, amax: torch.Tensor, out=None):
@@ -142,8 +287,56 @@ def moe_combine(y: torch.Tensor, topk_weights: torch.Tensor, topk: int, out_dtyp
     return out
 
 
+def moe_block_m(dtype: int, M: int, E: int, topk: int) -> int:
+    """Rows per tile (block_m) the fused layer aligns such a batch to; 0 for invalid arguments."""
+    return lib().moe_block_m(dtype, M, E, topk)
+
+
 def fused_moe_workspace_size(dtype: int, M: int, E: int, topk: int, H: int, I: int) -> int:
     return lib().fused_moe_workspace_size(dtype, M, E, topk, H, I)
+
+
+def _check_block_layer(x, w1, w2, w1_scale, w2_scale) -> None:
+    """Operands of a layer on block-scaled e4m3 weights."""
+    E, twoI, H = w1.shape
+    dev, I = w1.device, twoI // 2
+    _need("x", x, (torch.bfloat16,), (x.shape[0], H), dev)
+    _need("w1", w1, _F8, (E, 2 * I, H), dev)
+    _need("w2", w2, _F8, (E, H, I), dev)
+    _need("w1_scale", w1_scale, _F32, (E, 2 * I // 128, H // 128), dev)
+    _need("w2_scale", w2_scale, _F32, (E, H // 128, I // 128), dev)
+
+
+def fused_moe_grouped(x, router_logits, w1, w2, topk: int, routing: Routing, x_scale=None, w1_scale=None,
+                      w2_scale=None, workspace=None, out=None, topk_ids=None, topk_weights=None):
+    """The whole layer with a grouped router (float32 logits); returns out[M,H]
+    (float32 for fp32 weights, bfloat16 otherwise)."""
+    M, H = x.shape
+    E, twoI, _ = w1.shape
+    I = twoI // 2
+    dev = x.device
+    stream = _stream(x)
+    dt = _layer_dtype(w1, w1_scale)
+    if dt == MOE_FP8_BLOCK:
+        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
+    _need("router_logits", router_logits, _F32, (M, E), dev)
+    routing._check(E, dev)
+    if workspace is None:
+        need = fused_moe_workspace_size(dt, M, E, topk, H, I)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty((M, H), dtype=_INTER[dt], device=dev)
+    _need("out", out, (_INTER[dt],), (M, H), dev)
+    if topk_ids is not None:
+        _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
+    if topk_weights is not None:
+        _need("topk_weights", topk_weights, _F32, (M, topk), dev)
+    with _on(x):
+        check(lib().fused_moe_grouped(dt, _p(x), _p(x_scale), _p(router_logits), routing._ref, _p(w1), _p(w1_scale),
+                                      _p(w2), _p(w2_scale), M, E, topk, H, I, _p(out), _p(topk_ids),
+                                      _p(topk_weights), _p(workspace), workspace.numel(), stream),
+              "fused_moe_grouped")
+    return out
 
 
 def fused_moe(x, router_logits, w1, w2, topk: int, renormalize: bool = True, x_scale=None, w1_scale=None,
@@ -152,7 +345,9 @@ def fused_moe(x, router_logits, w1, w2, topk: int, renormalize: bool = True, x_s
     M, H = x.shape
     E, twoI, _ = w1.shape
     I = twoI // 2
-    dt = moe_dtype(w1)
+    dt = _layer_dtype(w1, w1_scale)
+    if dt == MOE_FP8_BLOCK:
+        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
     need = fused_moe_workspace_size(dt, M, E, topk, H, I)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
@@ -171,7 +366,9 @@ def fused_moe_noalloc(x, router_logits, w1, w2, topk: int, renormalize: bool = T
     M, H = x.shape
     E, twoI, _ = w1.shape
     I = twoI // 2
-    dt = moe_dtype(w1)
+    dt = _layer_dtype(w1, w1_scale)
+    if dt == MOE_FP8_BLOCK:
+        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
     if out is None:
         out = torch.empty((M, H), dtype=_INTER[dt], device=x.device)
     check(lib().fused_moe_noalloc(dt, _p(x), _p(x_scale), _p(router_logits), _p(w1), _p(w1_scale), _p(w2),
@@ -200,7 +397,9 @@ def fused_moe_router(x, router_w, w1, w2, topk: int, renormalize: bool = True, x
     M, H = x.shape
     E, twoI, _ = w1.shape
     I = twoI // 2
-    dt = moe_dtype(w1)
+    dt = _layer_dtype(w1, w1_scale)
+    if dt == MOE_FP8_BLOCK:
+        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
     need = fused_moe_workspace_size(dt, M, E, topk, H, I)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
@@ -227,7 +426,7 @@ class ExpertCache:
     memory unless already pinned."""
 
     def __init__(self, w1, w2, capacity: int, w1_scale=None, w2_scale=None, device=None, copy_stream=None):
-        self.dtype = moe_dtype(w1)
+        self.dtype = _layer_dtype(w1, w1_scale)
         self.E, twoI = w1.shape[0], w1.shape[1]
         self.I, self.H, self.capacity = twoI // 2, w2.shape[1], capacity
         device = torch.device("cuda" if device is None else device)

@@ -9,8 +9,9 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 (MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_ALIGNMENT, MOE_ERR_HIP,
  MOE_ERR_SCRATCH) = range(8)
-MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_W4A16 = 0, 1, 2, 3
-MOE_GEMM_GATE_UP_SILU, MOE_GEMM_DOWN, MOE_GEMM_DOWN_E4M3_ACT = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_W4A16, MOE_FP8_BLOCK = 0, 1, 2, 3, 4
+MOE_GEMM_GATE_UP_SILU, MOE_GEMM_DOWN, MOE_GEMM_DOWN_E4M3_ACT, MOE_GEMM_GATE_UP_SILU_E4M3 = 0, 1, 2, 3
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
 class AlignBufs(ctypes.Structure):
@@ -20,6 +21,13 @@ class AlignBufs(ctypes.Structure):
 
 class ExpertWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "w2", "w1_scale", "w2_scale")]
+
+
+class RoutingArgs(ctypes.Structure):
+    """moe_routing"""
+    _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -34,15 +42,20 @@ _lib = None
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 SIGNATURES = {
     "moe_route": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_route_grouped": (ctypes.c_int, [ctypes.c_int, _P, ctypes.POINTER(RoutingArgs), _I32, _I32, _I32, _P, _P, _P]),
     "moe_align_capacity": (_I64, [_I32, _I32, _I32, _I32]),
     "moe_align": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, AlignBufs, _P]),
     "moe_grouped_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, ctypes.POINTER(AlignBufs),
                                         _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "moe_quant_act": (ctypes.c_int, [_P, _P, _I64, _P, _P]),
+    "moe_quant_block": (ctypes.c_int, [ctypes.c_int, _P, _I32, _I32, _I32, _P, _P, _P]),
     "moe_combine": (ctypes.c_int, [ctypes.c_int, _P, _P, _I32, _I32, _I32, ctypes.c_int, _P, _P]),
+    "moe_block_m": (_I32, [ctypes.c_int, _I32, _I32, _I32]),
     "fused_moe_workspace_size": (_SZ, [ctypes.c_int, _I32, _I32, _I32, _I32, _I32]),
     "fused_moe": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
                                  _P, _P, _P, _P, _SZ, _P]),
+    "fused_moe_grouped": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, ctypes.POINTER(RoutingArgs), _P, _P, _P, _P, _I32,
+                                         _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     "moe_router_logits": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, _I32, _I32, _I32, _P, _P]),
     "fused_moe_router": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                         _I32, _P, _P, _P, _P, _SZ, _P]),

@@ -69,6 +69,13 @@ void part_bytes(moe_dtype d, int64_t H, int64_t I, size_t b[4]) {
         b[3] = (size_t)(I / 128 * H * 4);
         return;
     }
+    if (d == MOE_FP8_BLOCK) {  // one code per weight, one float scale per 128 x 128 block
+        b[0] = (size_t)(2 * I * H);
+        b[1] = (size_t)(H * I);
+        b[2] = (size_t)(2 * I / 128 * (H / 128) * 4);
+        b[3] = (size_t)(H / 128 * (I / 128) * 4);
+        return;
+    }
     const size_t eb = d == MOE_F32 ? 4 : d == MOE_BF16 ? 2 : 1;
     b[0] = (size_t)(2 * I * H) * eb;
     b[1] = (size_t)(H * I) * eb;
@@ -156,12 +163,11 @@ moe_status moe_cache_create(moe_dtype dtype, int32_t E, int32_t H, int32_t I, in
                             moe_expert_cache** out) {
     if (!out) return MOE_ERR_NULL;
     *out = nullptr;
-    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_FP8_E4M3 && dtype != MOE_W4A16)
-        return MOE_ERR_UNSUPPORTED;
-    if (E < 1 || capacity < 1 || capacity > E || H < 1 || I < 1 || H % 128 || I % 128) return MOE_ERR_SHAPE;
-    if ((dtype == MOE_FP8_E4M3 || dtype == MOE_W4A16) && (H % 256 || I % 256)) return MOE_ERR_SHAPE;
+    if (!known_dtype(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (E < 1 || capacity < 1 || capacity > E || H < 1 || I < 1) return MOE_ERR_SHAPE;
+    if (H % dim_multiple(dtype) || I % dim_multiple(dtype)) return MOE_ERR_SHAPE;
     if (E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
-    const bool scaled = dtype == MOE_FP8_E4M3 || dtype == MOE_W4A16;
+    const bool scaled = scaled_weights(dtype);
     if (!host.w1 || !host.w2 || !slots.w1 || !slots.w2) return MOE_ERR_NULL;
     if (scaled && (!host.w1_scale || !host.w2_scale || !slots.w1_scale || !slots.w2_scale)) return MOE_ERR_NULL;
     if (!scaled && (host.w1_scale || host.w2_scale || slots.w1_scale || slots.w2_scale)) return MOE_ERR_UNSUPPORTED;

@@ -1,6 +1,7 @@
 // C ABI of the fused MoE layer: host-side validation (before any HIP call),
 // workspace carving and the launch sequence route -> align -> GATE_UP GEMM
 // -> DOWN GEMM -> combine (FusedMoE vs MegaMoE post, section 3.1).
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -29,20 +30,43 @@ moe_status check_router(int32_t M, int32_t E, int32_t topk) {
 
 bool valid_block_m(int32_t b) { return b == 1 || b == 16 || b == 32 || b == 64 || b == 128 || b == 256; }
 
-bool known_dtype(moe_dtype d) { return d == MOE_F32 || d == MOE_BF16 || d == MOE_FP8_E4M3 || d == MOE_W4A16; }
+moe_status check_routing(const moe_routing* r, int32_t E, int32_t topk) {
+    if (!r) return MOE_ERR_NULL;
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_UNSUPPORTED;
+    if (r->n_groups < 1 || E % r->n_groups || r->topk_groups < 1 || r->topk_groups > r->n_groups) return MOE_ERR_SHAPE;
+    const int32_t gs = E / r->n_groups;
+    if ((r->group_top != 1 && r->group_top != 2) || r->group_top > gs || topk > r->topk_groups * gs)
+        return MOE_ERR_SHAPE;
+    if (!isfinite(r->scale)) return MOE_ERR_SHAPE;
+    if (r->n_groups > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(r->bias) & 3u) return MOE_ERR_ALIGNMENT;
+    return MOE_OK;
+}
 
-// layer dtypes whose weights carry scales (fp8: one per expert matrix; W4A16: per group)
-bool scaled_weights(moe_dtype d) { return d == MOE_FP8_E4M3 || d == MOE_W4A16; }
+static RouteSpec route_spec(const moe_routing& r) {
+    return RouteSpec{(int)r.score, r.bias, r.n_groups, r.topk_groups, r.group_top, r.renormalize, r.scale};
+}
+
+bool known_dtype(moe_dtype d) {
+    return d == MOE_F32 || d == MOE_BF16 || d == MOE_FP8_E4M3 || d == MOE_W4A16 || d == MOE_FP8_BLOCK;
+}
+
+// layer dtypes whose weights carry scales (fp8: one per expert matrix; W4A16: per group; block fp8: per block)
+bool scaled_weights(moe_dtype d) { return d == MOE_FP8_E4M3 || d == MOE_W4A16 || d == MOE_FP8_BLOCK; }
+
+int dim_multiple(moe_dtype d) { return (d == MOE_FP8_E4M3 || d == MOE_W4A16) ? 256 : 128; }
 
 // bytes of an element of y: f32 for the f32 path, bf16 otherwise
 size_t inter_bytes(moe_dtype d) { return d == MOE_F32 ? 4 : 2; }
 // ... and of act: the e4m3 layer keeps it in float32 until it is quantised
+// (block fp8 layers pass float32 or codes, see block_f32_act)
 size_t act_bytes(moe_dtype d) { return (d == MOE_BF16 || d == MOE_W4A16) ? 2 : 4; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int32_t fused_block_m(moe_dtype dtype, int32_t M, int32_t E, int32_t topk) {
     if (dtype == MOE_F32 || dtype == MOE_W4A16) return 16;  // decode kernels only
+    if (dtype == MOE_FP8_BLOCK) return block_tile_rows(M, E, topk);
     const char* env = getenv("MOE_GEMM_PATH");
     if (env && strcmp(env, "prefill") == 0) return 64;
     if (env && strcmp(env, "decode") == 0) return 16;
@@ -91,12 +115,20 @@ FusedLayout fused_layout(char* ws, moe_dtype dtype, int32_t M, int32_t E, int32_
     L.al.active_experts = c.take<int32_t>(P < E ? P : E);
     L.al.num_active = c.take<int32_t>(1);
     L.amax = c.take<float>(1);
-    L.act = c.take<char>((size_t)P * I * act_bytes(dtype));
+    const bool blk = dtype == MOE_FP8_BLOCK;
+    const bool codes = blk && !block_f32_act(M, E, topk, H, I);  // the GEMMs pass act as codes and scales
+    L.xq = blk ? c.take<char>((size_t)M * H) : nullptr;
+    L.xs = blk ? c.take<float>((size_t)M * (H / 128)) : nullptr;
+    L.act_s = codes ? c.take<float>((size_t)P * (I / 128)) : nullptr;
+    L.act = c.take<char>((size_t)P * I * (codes ? 1 : act_bytes(dtype)));
     L.dc = down_combine_fits(dtype, M, topk, E, H, I, L.block_m);
     L.y = L.dc ? nullptr : c.take<char>((size_t)P * H * inter_bytes(dtype));
     L.q_on_load = dtype == MOE_FP8_E4M3 && fp8_down_quantises_on_load(M, topk, E, H, I, L.block_m);
     L.act_q = (dtype == MOE_FP8_E4M3 && !L.q_on_load) ? c.take<char>((size_t)P * I) : nullptr;
-    L.ksplit = L.dc ? 1 : down_ksplit(dtype, M, topk, E, H, I, L.block_m);
+    if (blk)
+        L.ksplit = codes ? 1 : block_down_ksplit(M, topk, E, H, I);
+    else
+        L.ksplit = L.dc ? 1 : down_ksplit(dtype, M, topk, E, H, I, L.block_m);
     L.ypart = L.ksplit > 1 ? c.take<float>((size_t)L.ksplit * P * H) : nullptr;
     // one e4m3 token (the GEMMs may route it themselves): the intermediate's
     // amax as partials, one per 32 gate/up output columns of each slot
@@ -135,6 +167,19 @@ moe_status moe_route(const float* logits, int32_t M, int32_t E, int32_t topk, in
                                    static_cast<hipStream_t>(stream)));
 }
 
+moe_status moe_route_grouped(moe_dtype logits_dtype, const void* logits, const moe_routing* routing, int32_t M,
+                             int32_t E, int32_t topk, int32_t* topk_ids, float* topk_weights, void* stream) {
+    if (logits_dtype != MOE_F32 && logits_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    moe_status st = check_router(M, E, topk);
+    if (st == MOE_OK) st = check_routing(routing, E, topk);
+    if (st != MOE_OK) return st;
+    if (M == 0) return MOE_OK;
+    if (!logits || !topk_ids || !topk_weights) return MOE_ERR_NULL;
+    if (misaligned(logits) || misaligned(topk_ids) || misaligned(topk_weights)) return MOE_ERR_ALIGNMENT;
+    return hip_status(launch_route_grouped(logits_dtype, logits, route_spec(*routing), M, E, topk, topk_ids,
+                                           topk_weights, static_cast<hipStream_t>(stream)));
+}
+
 int64_t moe_align_capacity(int32_t M, int32_t topk, int32_t E, int32_t block_m) {
     if (M < 0 || topk < 1 || E < 1 || block_m < 1) return -1;
     const int64_t P = (int64_t)M * topk;
@@ -161,13 +206,43 @@ moe_status moe_align(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E
                                    static_cast<hipStream_t>(stream)));
 }
 
+// moe_grouped_gemm on MOE_FP8_BLOCK.
+static moe_status block_gemm(moe_gemm_kind kind, const void* a, const float* a_scale, const void* w,
+                             const float* w_scale, const moe_align_bufs* al, int32_t M, int32_t topk, int32_t E,
+                             int32_t N, int32_t K, int32_t block_m, void* c, float* c_scale, hipStream_t s) {
+    const bool gate = kind == MOE_GEMM_GATE_UP_SILU || kind == MOE_GEMM_GATE_UP_SILU_E4M3;
+    const bool tiles = kind == MOE_GEMM_GATE_UP_SILU_E4M3 || kind == MOE_GEMM_DOWN_E4M3_ACT;
+    moe_status st = check_router(M, E, topk);
+    if (st != MOE_OK) return st;
+    if (N < 1 || K < 1 || N % (gate ? 256 : 128) || K % 128) return MOE_ERR_SHAPE;
+    if (!valid_block_m(block_m) || (tiles && !block_tile_rows_ok(block_m))) return MOE_ERR_UNSUPPORTED;
+    if ((uint64_t)N * (uint64_t)K > 0xffffffffull) return MOE_ERR_UNSUPPORTED;
+    if ((kind == MOE_GEMM_DOWN && a_scale) || (kind != MOE_GEMM_GATE_UP_SILU_E4M3 && c_scale))
+        return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    if (!a || !w || !w_scale || !al || !c || !al->sorted_ids || !al->tile_expert || !al->expert_counts ||
+        !al->expert_offsets || !al->active_experts || !al->num_active)
+        return MOE_ERR_NULL;
+    if ((kind != MOE_GEMM_DOWN && !a_scale) || (kind == MOE_GEMM_GATE_UP_SILU_E4M3 && !c_scale)) return MOE_ERR_NULL;
+    if (misaligned(a) || misaligned(a_scale) || misaligned(w) || misaligned(w_scale) || misaligned(c) ||
+        misaligned(c_scale))
+        return MOE_ERR_ALIGNMENT;
+    return hip_status(launch_block_gemm(
+        BlockGemmCall{kind, a, a_scale, w, w_scale, *al, M, topk, E, N, K, block_m, c, c_scale}, s));
+}
+
 moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, const float* a_scale,
                             const void* w, const float* w_scale, const moe_align_bufs* al, int32_t M,
                             int32_t topk, int32_t E, int32_t N, int32_t K, int32_t block_m, void* c,
                             float* c_amax, void* stream) {
-    if (kind != MOE_GEMM_GATE_UP_SILU && kind != MOE_GEMM_DOWN && kind != MOE_GEMM_DOWN_E4M3_ACT)
+    if (kind != MOE_GEMM_GATE_UP_SILU && kind != MOE_GEMM_DOWN && kind != MOE_GEMM_DOWN_E4M3_ACT &&
+        kind != MOE_GEMM_GATE_UP_SILU_E4M3)
         return MOE_ERR_UNSUPPORTED;
     if (!known_dtype(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (dtype == MOE_FP8_BLOCK)
+        return block_gemm(kind, a, a_scale, w, w_scale, al, M, topk, E, N, K, block_m, c, c_amax,
+                          static_cast<hipStream_t>(stream));
+    if (kind == MOE_GEMM_GATE_UP_SILU_E4M3) return MOE_ERR_UNSUPPORTED;
     if (kind == MOE_GEMM_DOWN_E4M3_ACT && dtype != MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
     const bool act_q8 = kind == MOE_GEMM_DOWN_E4M3_ACT;
     if (act_q8) kind = MOE_GEMM_DOWN;
@@ -204,6 +279,17 @@ moe_status moe_quant_act(const void* act, const float* amax, int64_t n, void* ac
     return hip_status(launch_quant_act(act, amax, act_q, (size_t)n, static_cast<hipStream_t>(stream)));
 }
 
+moe_status moe_quant_block(moe_dtype x_dtype, const void* x, int32_t rows, int32_t K, int32_t block_rows, void* q,
+                           float* scale, void* stream) {
+    if (x_dtype != MOE_F32 && x_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (rows < 0 || K < 1 || K % 128) return MOE_ERR_SHAPE;
+    if (block_rows != 1 && block_rows != 128) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale) return MOE_ERR_NULL;
+    if (misaligned(x) || misaligned(q) || misaligned(scale)) return MOE_ERR_ALIGNMENT;
+    return hip_status(launch_quant_block(x_dtype, x, rows, K, block_rows, q, scale, static_cast<hipStream_t>(stream)));
+}
+
 moe_status moe_combine(moe_dtype y_dtype, const void* y, const float* topk_weights, int32_t M,
                        int32_t topk, int32_t H, moe_dtype out_dtype, void* out, void* stream) {
     if ((y_dtype != MOE_F32 && y_dtype != MOE_BF16) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16))
@@ -215,6 +301,11 @@ moe_status moe_combine(moe_dtype y_dtype, const void* y, const float* topk_weigh
     if (misaligned(y) || misaligned(out)) return MOE_ERR_ALIGNMENT;
     return hip_status(launch_combine(y_dtype, y, topk_weights, M, topk, H, out_dtype, out,
                                      static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_block_m(moe_dtype dtype, int32_t M, int32_t E, int32_t topk) {
+    if (!known_dtype(dtype) || M < 1 || check_router(M, E, topk) != MOE_OK) return 0;
+    return fused_block_m(dtype, M, E, topk);
 }
 
 size_t fused_moe_workspace_size(moe_dtype dtype, int32_t M, int32_t E, int32_t topk, int32_t H, int32_t I) {
@@ -234,9 +325,9 @@ moe_status check_fused(moe_dtype dtype, const void* x, const float* x_scale, con
     if (!known_dtype(dtype)) return MOE_ERR_UNSUPPORTED;
     moe_status st = check_router(M, E, topk);
     if (st != MOE_OK) return st;
-    if (H < 1 || I < 1 || H % 128 || I % 128) return MOE_ERR_SHAPE;
-    const bool fp8 = dtype == MOE_FP8_E4M3, w4 = dtype == MOE_W4A16;
-    if ((fp8 || w4) && (H % 256 || I % 256)) return MOE_ERR_SHAPE;
+    if (H < 1 || I < 1 || H % dim_multiple(dtype) || I % dim_multiple(dtype)) return MOE_ERR_SHAPE;
+    const bool fp8 = dtype == MOE_FP8_E4M3;
+    if (dtype == MOE_FP8_BLOCK && 2ull * (uint64_t)I * (uint64_t)H > 0xffffffffull) return MOE_ERR_UNSUPPORTED;
     if (!fp8 && x_scale) return MOE_ERR_UNSUPPORTED;
     if (!scaled_weights(dtype) && (w1_scale || w2_scale)) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
@@ -258,6 +349,18 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
                        const float* route_logits, int32_t renormalize, int32_t* route_ids) {
     const bool fp8 = dtype == MOE_FP8_E4M3;
     const moe_dtype inter = dtype == MOE_F32 ? MOE_F32 : MOE_BF16;
+    if (dtype == MOE_FP8_BLOCK) {
+        const bool codes = L.act_s != nullptr;
+        if (launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess) return MOE_ERR_HIP;
+        const BlockGemmCall b1{codes ? MOE_GEMM_GATE_UP_SILU_E4M3 : MOE_GEMM_GATE_UP_SILU, L.xq, L.xs, w1, w1_scale,
+                               L.al, M, topk, E, 2 * I, H, L.block_m, L.act, L.act_s};
+        if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
+        const BlockGemmCall b2{codes ? MOE_GEMM_DOWN_E4M3_ACT : MOE_GEMM_DOWN, L.act, L.act_s, w2, w2_scale,
+                               L.al, M, topk, E, H, I, L.block_m, L.y, nullptr, L.ksplit, L.ypart};
+        if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
+        if (L.ksplit > 1) return hip_status(launch_combine_partials(L.ypart, L.ksplit, wts, M, topk, H, inter, out, s));
+        return hip_status(launch_combine(inter, L.y, wts, M, topk, H, inter, out, s));
+    }
     GemmCall g1{MOE_GEMM_GATE_UP_SILU, dtype, x, x_scale, w1, w1_scale, L.al, M, topk, E, 2 * I, H,
                 L.block_m, L.act, fp8 ? L.amax : nullptr};
     // route_logits: the GEMMs route the one token themselves; the gate/up
@@ -307,14 +410,22 @@ static bool self_route_fits(moe_dtype dtype, int32_t M, int32_t E, int32_t topk,
 // x . router_w^T (in the same launch as route + align when that fits).
 moe_status run_fused(moe_dtype dtype, const void* x, const float* x_scale, const float* router_logits,
                      const void* w1, const float* w1_scale, const void* w2, const float* w2_scale, int32_t M,
-                     int32_t E, int32_t topk, int32_t H, int32_t I, int32_t renormalize, void* out,
+                     int32_t E, int32_t topk, int32_t H, int32_t I, FusedRoute route, void* out,
                      int32_t* topk_ids_out, float* topk_weights_out, const FusedLayout& L, hipStream_t s,
                      const float* router_w = nullptr) {
+    const int32_t renormalize = route.renormalize;
     const bool fp8 = dtype == MOE_FP8_E4M3;
     int32_t* ids = topk_ids_out ? topk_ids_out : L.ids;
     float* wts = topk_weights_out ? topk_weights_out : L.wts;
     float* logits = const_cast<float*>(router_logits);
-    const moe_dtype xdt = dtype == MOE_W4A16 ? MOE_BF16 : dtype;  // the activations' storage
+    // the activations' storage
+    const moe_dtype xdt = (dtype == MOE_W4A16 || dtype == MOE_FP8_BLOCK) ? MOE_BF16 : dtype;
+    if (route.spec) {
+        if (launch_route_grouped(MOE_F32, logits, *route.spec, M, E, topk, ids, wts, s) != hipSuccess ||
+            launch_align(ids, M, topk, E, L.block_m, L.cap, L.al, fp8 ? L.amax : nullptr, s) != hipSuccess)
+            return MOE_ERR_HIP;
+        return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s);
+    }
     if (self_route_fits(dtype, M, E, topk, H, I, L)) {
         // one token on the decode kernels: they route it themselves, so the
         // layer needs no route / align launch (the launch and its dependent
@@ -400,8 +511,26 @@ moe_status fused_moe(moe_dtype dtype, const void* x, const float* x_scale, const
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MOE_ERR_ALIGNMENT;
     FusedLayout L = fused_layout(static_cast<char*>(workspace), dtype, M, E, topk, H, I);
     if (workspace_bytes < L.bytes) return MOE_ERR_WORKSPACE;
-    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, renormalize, out,
-                     topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream));
+    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, FusedRoute{renormalize, nullptr},
+                     out, topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream));
+}
+
+moe_status fused_moe_grouped(moe_dtype dtype, const void* x, const float* x_scale, const float* router_logits,
+                             const moe_routing* routing, const void* w1, const float* w1_scale, const void* w2,
+                             const float* w2_scale, int32_t M, int32_t E, int32_t topk, int32_t H, int32_t I,
+                             void* out, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    moe_status st = check_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out,
+                                topk_ids_out, topk_weights_out);
+    if (st == MOE_OK) st = check_routing(routing, E, topk);
+    if (st != MOE_OK || M == 0) return st;
+    if (!workspace) return MOE_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MOE_ERR_ALIGNMENT;
+    FusedLayout L = fused_layout(static_cast<char*>(workspace), dtype, M, E, topk, H, I);
+    if (workspace_bytes < L.bytes) return MOE_ERR_WORKSPACE;
+    const RouteSpec spec = route_spec(*routing);
+    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I,
+                     FusedRoute{1, &spec}, out, topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_router_logits(moe_dtype x_dtype, const void* x, const float* x_scale, const float* router_w,
@@ -429,8 +558,8 @@ moe_status fused_moe_router(moe_dtype dtype, const void* x, const float* x_scale
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MOE_ERR_ALIGNMENT;
     FusedLayout L = fused_layout(static_cast<char*>(workspace), dtype, M, E, topk, H, I);
     if (workspace_bytes < L.bytes) return MOE_ERR_WORKSPACE;
-    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, renormalize, out,
-                     topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream), router_w);
+    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, FusedRoute{renormalize, nullptr},
+                     out, topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream), router_w);
 }
 
 size_t fused_moe_noalloc_scratch_bytes(void) { return kScratchBytes; }
@@ -448,8 +577,8 @@ moe_status fused_moe_noalloc(moe_dtype dtype, const void* x, const float* x_scal
     void* ws = scratch_for_current_device(&err);
     if (!ws) return MOE_ERR_HIP;
     FusedLayout L = fused_layout(static_cast<char*>(ws), dtype, M, E, topk, H, I);
-    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, renormalize, out,
-                     topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream));
+    return run_fused(dtype, x, x_scale, router_logits, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, FusedRoute{renormalize, nullptr},
+                     out, topk_ids_out, topk_weights_out, L, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "moe.h"
+#include "moe_launch.h"
 
 namespace moe {
 
@@ -26,9 +27,19 @@ struct FusedLayout {
     bool dc;         // the DOWN kernel also combines (no y, no combine launch)
     void* act_q;     // fp8 otherwise: e4m3 codes of act
     float* ypart;
+    char* xq;        // MOE_FP8_BLOCK: e4m3 codes of x [M][H]
+    float* xs;       // ... and their scales [M][H/128]
+    float* act_s;    // ... scales of the e4m3 act [P][I/128] (NULL: act is float32)
     float* amax;
     float* amax_parts;  // e4m3, one token: partial maxima of act ([topk][I/32]), see GemmCall
     int32_t amax_nparts;
+};
+
+// The routing a layer runs: the plain softmax top-k (spec NULL), or a grouped
+// router's.
+struct FusedRoute {
+    int32_t renormalize;
+    const RouteSpec* spec;
 };
 
 // ws == nullptr: only the sizes (L.bytes).  E: the experts the weights hold.
@@ -37,6 +48,11 @@ FusedLayout fused_layout(char* ws, moe_dtype dtype, int32_t M, int32_t E, int32_
 bool misaligned(const void* p);
 moe_status hip_status(hipError_t e);
 moe_status check_router(int32_t M, int32_t E, int32_t topk);
+moe_status check_routing(const moe_routing* r, int32_t E, int32_t topk);
+
+bool known_dtype(moe_dtype d);
+bool scaled_weights(moe_dtype d);  // weights that carry scales
+int dim_multiple(moe_dtype d);     // what H and I must be multiples of
 
 // Argument checks of fused_moe (host only; router_logits may be an output).
 moe_status check_fused(moe_dtype dtype, const void* x, const float* x_scale, const float* router_logits,

@@ -12,6 +12,7 @@ namespace moe {
 // Limits the ABI enforces (the kernels size LDS tables and unrolled loops by them).
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopk = 16;
+constexpr int kMaxGroups = 64;  // groups of experts (one lane each)
 constexpr int kMaxKsplit = 8;  // K split of the decode DOWN GEMM (float32 partials)
 
 // Which grouped-GEMM kernel family serves a call.
@@ -22,6 +23,16 @@ hipError_t launch_route(const float* logits, int M, int E, int topk, int renorma
 
 hipError_t launch_align(const int32_t* ids, int M, int topk, int E, int block_m, int64_t cap,
                         const moe_align_bufs& out, float* zero_f32, hipStream_t s);
+
+// A grouped router's choice and weights (moe_routing, by value for kernels).
+struct RouteSpec {
+    int score;
+    const float* bias;
+    int n_groups, topk_groups, group_top, renormalize;
+    float scale;
+};
+hipError_t launch_route_grouped(moe_dtype ldt, const void* logits, const RouteSpec& r, int M, int E, int topk,
+                                int32_t* ids, float* weights, hipStream_t s);
 
 // Both steps in one launch for M <= 16 (one wavefront routes each token).
 bool route_align_fits(int M);
@@ -99,6 +110,34 @@ bool fp8_down_quantises_on_load(int M, int topk, int E, int N, int K, int block_
 
 // e4m3 codes of n float32 intermediate values (n a multiple of 16), scale amax/448.
 hipError_t launch_quant_act(const void* act, const float* amax, void* q, size_t n, hipStream_t s);
+
+// Block-scaled e4m3 codes and scales of x [rows][K] (float32 or bfloat16).
+hipError_t launch_quant_block(moe_dtype xdt, const void* x, int rows, int K, int block_rows, void* q, float* scale,
+                              hipStream_t s);
+
+// A grouped GEMM on block-scaled e4m3 (MOE_FP8_BLOCK); the kinds pick the
+// kernels: float32 act -> the ring kernel, e4m3 act -> the tile kernel.
+struct BlockGemmCall {
+    moe_gemm_kind kind;
+    const void* a;
+    const float* a_scale;
+    const void* w;
+    const float* w_scale;
+    moe_align_bufs al;
+    int M, topk, E, N, K, block_m;
+    void* c;
+    float* c_scale;          // GATE_UP_SILU_E4M3: scales of the codes c
+    int ksplit = 1;          // DOWN over float32 act: split of K across workgroups
+    float* cpart = nullptr;  // with ksplit > 1: float32 partials [ksplit][P][N] instead of c
+};
+hipError_t launch_block_gemm(const BlockGemmCall& g, hipStream_t s);
+
+// MOE_FP8_BLOCK layers: tile height, whether the GEMMs pass the intermediate
+// in float32 (ring kernels), and then the K split of the down GEMM.
+int block_tile_rows(int M, int E, int topk);
+bool block_tile_rows_ok(int block_m);
+bool block_f32_act(int M, int E, int topk, int H, int I);
+int block_down_ksplit(int M, int topk, int E, int N, int K);
 
 hipError_t launch_combine_partials(const float* ypart, int ksplit, const float* w, int M, int topk, int H,
                                    moe_dtype out_dtype, void* out, hipStream_t s);

@@ -90,6 +90,13 @@ __device__ __forceinline__ void lds_dma16_nt_at(const void* src, unsigned lds_ad
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "s"(m0) : "memory", "m0");
 }
 
+// 4 bytes per lane from global memory into LDS, at consecutive words from the
+// wave-uniform LDS byte address.
+__device__ __forceinline__ void lds_dma4_at(const void* src, unsigned lds_addr) {
+    const unsigned m0 = __builtin_amdgcn_readfirstlane(lds_addr);
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(m0) : "memory", "m0");
+}
+
 // Buffer-addressed copies into LDS: a raw (stride 0) buffer resource over
 // [base, base + bytes) plus a 32-bit per-lane offset (VGPR) and a wave-uniform
 // one (SGPR).  Reads past `bytes` return zeros instead of touching memory.

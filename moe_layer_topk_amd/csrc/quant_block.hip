@@ -1,0 +1,103 @@
+// Block-scaled e4m3 quantisation (moe_quant_block): per block of rows x 128
+// values s = max(amax / 448, 2^-126) and codes e4m3(x / s).
+#include "moe_block.h"
+#include "moe_launch.h"
+
+namespace moe {
+
+// Eight consecutive values of x as float32 bits; i a multiple of 8.
+template <int XDT>
+__device__ __forceinline__ void load8(const void* x, size_t i, float (&v)[8]) {
+    if constexpr (XDT == MOE_F32) {
+        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ unsigned amax8(const float (&v)[8]) {
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    return m;
+}
+
+// One scale per 128 values of a row: 16 lanes hold a block, 8 values each.
+template <int XDT>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const void* __restrict__ x, size_t nblk,
+                                                         uint8_t* __restrict__ q, float* __restrict__ scale) {
+    const int l = threadIdx.x & 15;
+    for (size_t b = (size_t)blockIdx.x * 16 + (threadIdx.x >> 4); b < nblk; b += (size_t)gridDim.x * 16) {
+        float v[8];
+        load8<XDT>(x, b * 128 + 8 * l, v);
+        const BlockQuant bq(row16_max_u32(amax8(v)));
+        *reinterpret_cast<uint2*>(q + b * 128 + 8 * l) =
+            uint2{bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
+        if (l == 0) scale[b] = bq.scale;
+    }
+}
+
+// One scale per 128 x 128 block: a workgroup per block, thread (r, l) holds 8
+// values of rows r, r + 16, ..., r + 112.
+template <int XDT>
+__global__ void __launch_bounds__(256) quant_tile_kernel(const void* __restrict__ x, int rows, int K,
+                                                         uint8_t* __restrict__ q, float* __restrict__ scale) {
+    __shared__ unsigned wmax[4];
+    const int nkb = K / 128;
+    const int r0 = (int)(blockIdx.x / nkb) * 128, l = threadIdx.x & 15, rr = threadIdx.x >> 4;
+    const size_t col = (size_t)(blockIdx.x % nkb) * 128 + 8 * l;
+    float v[8][8];
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + rr + 16 * i;
+        if (r < rows) {
+            load8<XDT>(x, (size_t)r * K + col, v[i]);
+            m = max(m, amax8(v[i]));
+        }
+    }
+    m = wave_max_u32(m);
+    if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+    __syncthreads();
+    const BlockQuant bq(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + rr + 16 * i;
+        if (r < rows)
+            *reinterpret_cast<uint2*>(q + (size_t)r * K + col) =
+                uint2{bq.pack4(v[i][0], v[i][1], v[i][2], v[i][3]), bq.pack4(v[i][4], v[i][5], v[i][6], v[i][7])};
+    }
+    if (threadIdx.x == 0) scale[blockIdx.x] = bq.scale;
+}
+
+template <int XDT>
+static hipError_t launch_x(const void* x, int rows, int K, int block_rows, void* q, float* scale, hipStream_t s) {
+    if (block_rows == 1) {
+        const size_t nblk = (size_t)rows * (K / 128);
+        const size_t blocks = (nblk + 15) / 16;
+        hipLaunchKernelGGL((quant_rows_kernel<XDT>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, x, nblk,
+                           static_cast<uint8_t*>(q), scale);
+    } else {
+        hipLaunchKernelGGL((quant_tile_kernel<XDT>), dim3((unsigned)((size_t)(K / 128) * (((size_t)rows + 127) / 128))), dim3(256), 0, s, x, rows, K,
+                           static_cast<uint8_t*>(q), scale);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_quant_block(moe_dtype xdt, const void* x, int rows, int K, int block_rows, void* q, float* scale,
+                              hipStream_t s) {
+    if (rows == 0) return hipSuccess;
+    if (xdt == MOE_F32) return launch_x<MOE_F32>(x, rows, K, block_rows, q, scale, s);
+    return launch_x<MOE_BF16>(x, rows, K, block_rows, q, scale, s);
+}
+
+}  // namespace moe
