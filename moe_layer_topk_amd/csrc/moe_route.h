@@ -1,0 +1,397 @@
+// The grouped router of one token (moe_route_grouped), by one wavefront.
+//
+// Lane l holds the V = ceil(E / 64) (1, 2 or 4) consecutive experts V l ..
+// V l + V - 1, so lanes in order are experts in order and the lowest lane of a
+// ballot is the lowest index.  Steps: scores; group scores (the two best
+// choices of a group merge across its lanes); every group's rank among the
+// groups; a stable sort of the lane's V candidates; topk rounds that take the
+// best head of the 64 sorted lists and pop it.
+//
+// The choice has to be the one of float64 scores.  The float32 pass bounds its
+// own error: with eta the bound of one choice, two that differ by more than
+// 4 eta are ordered as in float64.  A token with a closer pair at a place that
+// matters (neighbours among the taken, the best one left, two groups) is done
+// again in float64; on normal logits about one token in a thousand.  Without
+// a bias experts are ranked by their logits, exactly, ties included.
+//   sigmoid: 1 / (1 + e), e = exp2(-l log2 e): the argument's rounding costs
+//     |l| 2^-24, the exponential 2^-23, and s (1 - s) |l| <= 0.23; with the sum
+//     and the reciprocal below 4 x 2^-24, plus the sum's with the bias.
+//   softmax: numerators (2 |l - m| + 2) 2^-24, their sum at most
+//     (2 ln E + 10) 2^-24 of itself: below 2^-19 of the largest probability.
+#pragma once
+
+#include "moe_device.h"
+#include "moe_launch.h"
+
+namespace moe {
+
+// ordered integer keys; 0 is left for "nothing here"
+template <typename T>
+struct RankKey;
+template <>
+struct RankKey<float> {
+    using key = unsigned;
+    __device__ static __forceinline__ key of(float v) { return order_key(v); }
+    __device__ static __forceinline__ key wave_max(key k) { return wave_max_u32(k); }
+    __device__ static __forceinline__ float value(key k) { return key_value(k); }
+};
+template <>
+struct RankKey<double> {
+    using key = unsigned long long;
+    __device__ static __forceinline__ key of(double v) {
+        const key b = (key)__double_as_longlong(v == 0.0 ? 0.0 : v);
+        return (b >> 63) ? ~b : (b | (1ull << 63));
+    }
+    __device__ static __forceinline__ key wave_max(key k) {
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            const key o = (key)__shfl_xor((long long)k, off, 64);
+            k = o > k ? o : k;
+        }
+        return k;
+    }
+    __device__ static __forceinline__ double value(key k) {
+        return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
+    }
+};
+
+// v of the lane whose number differs in bit `step` from this one's.  Steps 0
+// to 3 of float values are lane moves on the vector ALU: quad swaps, and
+// mirrors, which are the same thing once every smaller step has been merged.
+__device__ __forceinline__ float lane_swap(float v, int step) {
+    const int i = __float_as_int(v);
+    switch (step) {
+        case 0: return __int_as_float(__builtin_amdgcn_update_dpp(i, i, 0xB1, 0xF, 0xF, false));
+        case 1: return __int_as_float(__builtin_amdgcn_update_dpp(i, i, 0x4E, 0xF, 0xF, false));
+        case 2: return __int_as_float(__builtin_amdgcn_update_dpp(i, i, 0x141, 0xF, 0xF, false));
+        case 3: return __int_as_float(__builtin_amdgcn_update_dpp(i, i, 0x140, 0xF, 0xF, false));
+        default: return __shfl_xor(v, 1 << step, 64);
+    }
+}
+__device__ __forceinline__ double lane_swap(double v, int step) { return __shfl_xor(v, 1 << step, 64); }
+
+__device__ __forceinline__ float lane_read(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_read(double v, int lane) {
+    const long long b = __double_as_longlong(v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)b, lane), hi = (unsigned)__builtin_amdgcn_readlane((int)(b >> 32), lane);
+    return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+
+__device__ __forceinline__ float wave_max_f32(float v) { return key_value(wave_max_u32(order_key(v))); }
+
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int step = 0; step < 6; ++step) v += lane_swap(v, step);
+    return v;
+}
+
+// The V logits of this lane, NaN as -inf, lanes past E -inf.
+template <int V>
+__device__ __forceinline__ void load_logits(const void* logits, bool bf16, size_t row, int E, float (&l)[V]) {
+    const int e0 = V * (int)__lane_id();
+    const float ninf = -__builtin_inff();
+    if (V > 1 && E % V == 0) {
+        // whole vectors: row * E is a multiple of V too
+#pragma unroll
+        for (int q = 0; q < V; ++q) l[q] = ninf;
+        if (e0 < E) {
+            if (bf16) {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(logits) + row * E + e0;
+                if constexpr (V == 4) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(p);
+                    l[0] = __uint_as_float(w.x << 16);
+                    l[1] = __uint_as_float(w.x & 0xffff0000u);
+                    l[2] = __uint_as_float(w.y << 16);
+                    l[3] = __uint_as_float(w.y & 0xffff0000u);
+                } else if constexpr (V == 2) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+                    l[0] = __uint_as_float(w << 16);
+                    l[1] = __uint_as_float(w & 0xffff0000u);
+                }
+            } else {
+                const float* p = reinterpret_cast<const float*>(logits) + row * E + e0;
+                if constexpr (V == 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(p);
+                    l[0] = w.x; l[1] = w.y; l[2] = w.z; l[3] = w.w;
+                } else if constexpr (V == 2) {
+                    const float2 w = *reinterpret_cast<const float2*>(p);
+                    l[0] = w.x; l[1] = w.y;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            l[q] = ninf;
+            if (e0 + q < E)
+                l[q] = bf16 ? bf2f(reinterpret_cast<const uint16_t*>(logits)[row * E + e0 + q])
+                            : reinterpret_cast<const float*>(logits)[row * E + e0 + q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) l[q] = l[q] == l[q] ? l[q] : ninf;
+}
+
+// What a wavefront keeps over its tokens: the biases of its experts.
+template <int V>
+struct RouteBias {
+    float b[V];
+    float top;  // largest |bias|
+    __device__ __forceinline__ void load(const RouteSpec& r, int E) {
+        const int e0 = V * (int)__lane_id();
+        float m = 0.0f;
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            b[q] = (r.bias && e0 + q < E) ? r.bias[e0 + q] : 0.0f;
+            m = fmaxf(m, fabsf(b[q]));
+        }
+        top = r.bias ? wave_max_f32(m) : 0.0f;
+    }
+};
+
+// One pass in T.  Returns false (float only) if a choice was too close to
+// call; else lane j < topk holds the j-th expert in sel.
+template <typename T, int V>
+__device__ __forceinline__ bool route_choose(const RouteSpec& r, int E, int topk, const float (&l)[V],
+                                             const RouteBias<V>& rb, float m, int& sel) {
+    using RK = RankKey<T>;
+    using key = typename RK::key;
+    const int lane = __lane_id();
+    const int e0 = V * lane;
+    const T ninf = -(T)__builtin_inff();
+    constexpr bool f32 = sizeof(T) == 4;
+    const bool grouped = r.topk_groups < r.n_groups;
+    const bool biased = r.bias != nullptr;
+
+    T c[V];  // choices
+    float eta = 0.0f;
+#pragma unroll
+    for (int q = 0; q < V; ++q) c[q] = (T)l[q];
+    if (grouped || biased) {
+        if (r.score == MOE_SCORE_SIGMOID) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                if constexpr (f32) c[q] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[q]));
+                else c[q] = 1.0 / (1.0 + exp(-(double)l[q]));
+            }
+            eta = 2.38418579e-07f;  // 2^-22
+        } else {
+            T den = 0;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                // (an infinite maximum: 1 at it, 0 elsewhere; nothing above -inf: all 0)
+                if constexpr (f32) c[q] = l[q] == m ? 1.0f : __expf(l[q] - m);
+                else c[q] = l[q] == m ? 1.0 : exp((double)l[q] - (double)m);
+                if (m == -__builtin_inff() || e0 + q >= E) c[q] = 0;
+                den += c[q];
+            }
+            den = wave_sum(den);
+            const T inv = den > 0 ? 1 / den : 0;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                if constexpr (f32) c[q] *= inv;
+                else c[q] = den > 0 ? c[q] / den : 0.0;  // rounded once, as a quotient
+            }
+            eta = 1.90734863e-06f * (float)inv;  // 2^-19 of the largest
+        }
+        if (biased) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                c[q] += (T)rb.b[q];
+                c[q] = c[q] == c[q] ? c[q] : ninf;
+            }
+            eta += 5.96046448e-08f * (1.0f + rb.top);
+        }
+    }
+
+    bool live[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) live[q] = e0 + q < E;
+    bool close = false;
+    if (grouped) {
+        const int gs = E / r.n_groups;
+        const int lpg = gs / V;  // lanes of a group, if groups are whole lanes
+        const bool whole = gs % V == 0 && (lpg & (lpg - 1)) == 0;
+        T mine;  // lane g * stride: the score of group g
+        int stride;
+        if (whole) {
+            T a = ninf, b = ninf;  // the two best of the lane, then of the group
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const T lo = a < c[q] ? a : c[q];
+                a = a < c[q] ? c[q] : a;
+                b = b < lo ? lo : b;
+            }
+#pragma unroll
+            for (int step = 0; step < 6; ++step) {
+                if ((1 << step) < lpg) {
+                    const T oa = lane_swap(a, step), ob = lane_swap(b, step);
+                    const T lo = a < oa ? a : oa, hb = b < ob ? ob : b;
+                    a = a < oa ? oa : a;
+                    b = lo < hb ? hb : lo;
+                }
+            }
+            mine = r.group_top == 2 ? a + b : a;
+            stride = lpg;
+        } else {
+            mine = ninf;
+            stride = 1;
+            for (int g = 0; g < r.n_groups; ++g) {
+                key k[V];
+                key best = 0;
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const int e = e0 + q;
+                    k[q] = (e >= g * gs && e < (g + 1) * gs) ? RK::of(c[q]) : 0;
+                    best = k[q] > best ? k[q] : best;
+                }
+                const key first = RK::wave_max(best);
+                T sum = RK::value(first);
+                if (r.group_top == 2) {
+                    // the second best: without the lowest lane's lowest candidate that holds the best
+                    const int at = (int)__builtin_ctzll(__ballot(best == first));
+                    bool gone = lane != at;
+                    best = 0;
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        if (!gone && k[q] == first) {
+                            gone = true;
+                            k[q] = 0;
+                        }
+                        best = k[q] > best ? k[q] : best;
+                    }
+                    sum += RK::value(RK::wave_max(best));
+                }
+                if (lane == g) mine = sum;
+            }
+        }
+        mine = mine == mine ? mine : ninf;
+        const int g0 = lane / stride;  // this lane's group (lanes past the last: ignored)
+        int rank = 0;
+        for (int g = 0; g < r.n_groups; ++g) {
+            const T o = lane_read(mine, g * stride);
+            rank += (o > mine || (o == mine && g < g0)) ? 1 : 0;
+            if constexpr (f32) {
+                const float d = fabsf(o - mine);
+                close |= g != g0 && !(d > 8.0f * eta + 2.38418579e-07f * fabsf(o));
+            }
+        }
+        const bool group_lane = lane < r.n_groups * stride;
+        close = close && group_lane;
+        const uint64_t kept = __ballot(group_lane && rank < r.topk_groups);
+#pragma unroll
+        for (int q = 0; q < V; ++q) live[q] = live[q] && ((kept >> (((e0 + q) / gs) * stride)) & 1);
+    }
+
+    // the lane's candidates, best first, equal ones in index order (dead: key 0)
+    key k[V];
+    int idx[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        k[q] = live[q] ? RK::of(biased ? c[q] : (T)l[q]) : 0;
+        idx[q] = e0 + q;
+    }
+    auto order = [&](int x, int y) __attribute__((always_inline)) {
+        const bool sw = k[y] > k[x] || (k[y] == k[x] && idx[y] < idx[x]);
+        const key tk = sw ? k[x] : k[y];
+        const int ti = sw ? idx[x] : idx[y];
+        k[x] = sw ? k[y] : k[x];
+        idx[x] = sw ? idx[y] : idx[x];
+        k[y] = tk;
+        idx[y] = ti;
+    };
+    if constexpr (V == 2) order(0, 1);
+    if constexpr (V == 4) {
+        order(0, 1);
+        order(2, 3);
+        order(0, 2);
+        order(1, 3);
+        order(1, 2);
+    }
+    const float tol = 4.0f * eta;
+    T last = 0;
+    for (int j = 0; j < topk; ++j) {
+        const key best = RK::wave_max(k[0]);
+        const int at = (int)__builtin_ctzll(__ballot(k[0] == best));
+        const int e = __builtin_amdgcn_readlane(idx[0], at);
+        if (lane == j) sel = e;
+        if constexpr (f32) {
+            if (biased) {
+                const T v = RK::value(best);
+                close |= j > 0 && !(last - v > tol);
+                last = v;
+            }
+        }
+        if (lane == at) {
+#pragma unroll
+            for (int q = 0; q + 1 < V; ++q) {
+                k[q] = k[q + 1];
+                idx[q] = idx[q + 1];
+            }
+            k[V - 1] = 0;
+        }
+    }
+    if constexpr (f32) {
+        if (biased) {
+            const key best = RK::wave_max(k[0]);  // the best one left out
+            close |= best != 0 && !(last - RK::value(best) > tol);
+        }
+        return __ballot(close) == 0;
+    }
+    return true;
+}
+
+// Routes the token whose logits are l: lane j < topk ends with expert *sel and
+// weight *w.
+template <int V>
+__device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, int topk, const float (&l)[V],
+                                                    const RouteBias<V>& rb, int* sel_out, float* w_out) {
+    const int lane = __lane_id();
+    const float ninf = -__builtin_inff();
+    const bool soft = r.score == MOE_SCORE_SOFTMAX;
+    float m = 0.0f;
+    if (soft) {
+        m = l[0];
+#pragma unroll
+        for (int q = 1; q < V; ++q) m = fmaxf(m, l[q]);
+        m = wave_max_f32(m);
+    }
+    int sel = 0;
+    if (!route_choose<float, V>(r, E, topk, l, rb, m, sel)) route_choose<double, V>(r, E, topk, l, rb, m, sel);
+
+    // the chosen experts' scores, from their logits
+    float lj = 0.0f;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        const float v = __shfl(l[q], sel / V, 64);
+        lj = sel % V == q ? v : lj;
+    }
+    const bool mine = lane < topk;
+    float s = 0.0f;
+    if (mine) s = soft ? (m == ninf ? 0.0f : lj == m ? 1.0f : expf(lj - m)) : 1.0f / (1.0f + expf(-lj));
+    float den = 1.0f;
+    if (r.renormalize) {
+        den = wave_sum(s);
+        if (den < 1e-30f) {
+            // scores that float32 cannot hold: the quotients still can be
+            double d = 0.0;
+            if (mine) d = soft ? (m == ninf ? 0.0 : lj == m ? 1.0 : exp((double)lj - (double)m)) : 1.0 / (1.0 + exp(-(double)lj));
+            const double sum = wave_sum(d);
+            s = sum > 0.0 ? (float)(d / sum) : 0.0f;
+            den = 1.0f;
+        }
+    } else if (soft) {
+        den = 0.0f;
+#pragma unroll
+        for (int q = 0; q < V; ++q)
+            den += (V * lane + q < E) ? (l[q] == m ? 1.0f : expf(l[q] - m)) : 0.0f;
+        den = wave_sum(den);
+    }
+    *sel_out = sel;
+    *w_out = s / den * r.scale;
+}
+
+}  // namespace moe
