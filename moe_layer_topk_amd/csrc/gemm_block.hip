@@ -29,6 +29,7 @@ struct BlockArgs {
     float* c_scale;
     int ksplit;
     float* cpart;
+    const int32_t* ids;  // one token: its topk ids, read instead of the alignment
     bool one_tile;  // an expert averages at most 64 rows: weight tiles feed about one row tile
 };
 
@@ -54,10 +55,10 @@ struct BlockArgs {
 // to bfloat16 (exact) and multiplies those at half the rate with full float32
 // sums.
 
-template <int BM_, int WN_, int ST_>
+template <int BM_, int BN_, int WN_, int ST_>
 struct BtCfg {
-    static constexpr int BM = BM_, BN = 256, ST = ST_;
-    static constexpr int WM = 4, WN = WN_, Waves = WM * WN, Threads = 64 * Waves;  // waves: WM along weights, WN along tokens
+    static constexpr int BM = BM_, BN = BN_, ST = ST_;
+    static constexpr int WM = BN / 64, WN = WN_, Waves = WM * WN, Threads = 64 * Waves;  // waves: WM along weights, WN along tokens
     static constexpr int TM = BN / WM / 32, TN = BM / WN / 32;                     // 32 x 32 tiles per wave
     static constexpr int ABytes = BM * 128, BBytes = BN * 128, StageBytes = ABytes + BBytes;
     static constexpr int ALoads = BM / 8 / Waves, BLoads = BN / 8 / Waves;         // 1 KB copies per wave and stage
@@ -69,7 +70,7 @@ struct BtCfg {
     static constexpr int IdOff = RowOff + 64 * SWaves * 4;                         // [BM] pair ids
     static constexpr int AmaxOff = IdOff + BM * 4;                                 // [WM][BM]
     static constexpr int LdsBytes = AmaxOff + WM * BM * 4;
-    static constexpr int OutStride = 528;                                          // DOWN: bytes of a staged output row
+    static constexpr int OutStride = 2 * BN + 16;                                  // DOWN: bytes of a staged output row
     static_assert(ALoads * 8 * Waves == BM && BLoads * 8 * Waves == BN, "copy split");
     static_assert(TM == 2 && TN >= 1, "one gate and one up tile per wave");
     static_assert(BM * OutStride <= ScaleOff, "staged output rows");
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % C::WM, wn = wave / C::WM;
     const int K = g.K, N = g.N, I = N / 2, P = g.P, nk = K / 128;
-    const int n0 = ntile * (GATE ? 128 : 256);
+    const int n0 = ntile * (GATE ? 128 : C::BN);
     int* rows_s = reinterpret_cast<int*>(bt_lds + C::RowOff);
     int* ids_s = reinterpret_cast<int*>(bt_lds + C::IdOff);
 
@@ -160,25 +161,25 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
         bsrc[j] = (unsigned)row * (unsigned)K + (unsigned)ring_swz(lphys, r) * 16u;
     }
     const unsigned lds0 = lds_addr_of(bt_lds);
-    auto issue = [&](int kt) __attribute__((always_inline)) {
+    // copy j of stage kt (0 .. L - 1: tokens, then weights)
+    auto issue_one = [&](int kt, int j) __attribute__((always_inline)) {
         const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
         const unsigned koff = (unsigned)kt * 128u;
-#pragma unroll
-        for (int j = 0; j < C::ALoads; ++j) {
+        if (j < C::ALoads) {
             const unsigned d = st + (wave * C::ALoads + j) * 1024;
             if constexpr (FAR) lds_dma16_at(afar[j] + koff, d);
             else lds_dma16_buf(arsrc, asrc[j], koff, d);
-        }
-#pragma unroll
-        for (int j = 0; j < C::BLoads; ++j) {
-            const unsigned d = st + C::ABytes + (wave * C::BLoads + j) * 1024;
-            if constexpr (NTW) lds_dma16_buf_nt(brsrc, bsrc[j], koff, d);
-            else lds_dma16_buf(brsrc, bsrc[j], koff, d);
+        } else {
+            const unsigned d = st + C::ABytes + (wave * C::BLoads + j - C::ALoads) * 1024;
+            if constexpr (NTW) lds_dma16_buf_nt(brsrc, bsrc[j - C::ALoads], koff, d);
+            else lds_dma16_buf(brsrc, bsrc[j - C::ALoads], koff, d);
         }
     };
-    // scales of chunk c (blocks 8 c ..): part q of 8 holds tokens 8 (q SWaves + wave) ..
+    // scales of chunk c (blocks 8 c ..): part q of 8 holds tokens 8 (q SWaves +
+    // wave) ..; further waves repeat the first ones' copy (the same bytes to the
+    // same place), so that a stage has no branch and every wave counts alike
     auto issue_scales = [&](int c, int q) __attribute__((always_inline)) {
-        const int i = (q * C::SWaves + wave) * 8;
+        const int i = (q * C::SWaves + wave % C::SWaves) * 8;
         const int row = rows_s[i + (lane >> 3)];
         const int kb = min(8 * c + (lane & 7), nk - 1);
         lds_dma4_at(g.a_scale + (size_t)row * nk + kb, lds0 + C::ScaleOff + (c % 3) * C::SBuf + i * 32);
@@ -186,23 +187,22 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
     __syncthreads();
     // this wave's own loads above have to be done before its copies are counted
     wait_vm<0>();
-    const bool scaler = wave < C::SWaves;
-    if (scaler)
-        for (int q = 0; q < 8; ++q) issue_scales(0, q);
-    // a stage's copies: its operands, and (scaling waves) one part of the next chunk's scales
-    auto issue_all = [&](int kt) __attribute__((always_inline)) {
-        issue(kt);
-        if (scaler) issue_scales(kt / 8 + 1, kt % 8);
+    for (int q = 0; q < 8; ++q) issue_scales(0, q);
+    // copies [j0, j1) of stage kt; the last is one part of the next chunk's scales
+    auto issue = [&](int kt, int j0, int j1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < C::L; ++j)
+            if (j >= j0 && j < j1) issue_one(kt, j);
+        if (j0 <= C::L && C::L < j1) issue_scales(kt / 8 + 1, kt % 8);
     };
 #pragma unroll
     for (int s0 = 0; s0 < C::ST - 1; ++s0)
-        if (s0 < nk) issue_all(s0);
+        if (s0 < nk) issue(s0, 0, C::L + 1);
 
     // wave tile: rows of the weights (row operand), tokens (column operand)
     const int l31 = lane & 31, khalf = lane >> 5;
-    int wrow[C::TM], trow[C::TN];
-#pragma unroll
-    for (int i = 0; i < C::TM; ++i) wrow[i] = GATE ? 128 * i + 32 * wm + l31 : 64 * wm + 32 * i + l31;
+    // (GATE: rows 32 wm of the gate half and of the up half, DOWN: rows 64 wm)
+    int trow[C::TN];
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) trow[j] = (wn * C::TN + j) * 32 + l31;
     const int nreal = min(C::BM, g.offsets[e] + g.counts[e] - mtile * C::BM);
@@ -221,89 +221,139 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
+    // LDS offsets of this lane's 16-byte chunks.  The swizzle depends on bits 1-3
+    // of the row, which the 32-row tiles share, so a tile is a constant away.
+    // GATE: chunk 2 c + khalf of step c (16 k per lane half, two MFMAs);
+    // DOWN: chunks 4 c + 2 khalf + h, the two halves of a 64-k MFMA.
+    int off[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        off[c] = l31 * 128 + (ring_swz(GATE ? 2 * c + khalf : 4 * (c >> 1) + 2 * khalf + (c & 1), l31) << 4);
+    const int tbase = wn * C::TN * 4096, wbase = C::ABytes + (GATE ? wm * 4096 : wm * 8192);
+    constexpr int kWStep = GATE ? 128 * 128 : 4096;  // from a wave's first weight tile to its second
+
+    f32x16 d[C::TM][C::TN];  // the block's sums
+    float sp[C::TM][C::TN];  // ... and their scales
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) {
+            sp[i][j] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) d[i][j][v] = 0.0f;
+        }
+    auto add_block = [&](auto lt_tag) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < decltype(lt_tag)::value; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = __builtin_fmaf(d[i][j][v], sp[i][j], acc[i][j][v]);
+    };
+    // One stage.  The previous block's scaled sums join the accumulators right
+    // after the barrier, while this block's first fragments come from LDS; the
+    // next fragments are read (and GATE: converted) and the next stage's copies
+    // go out between the products.
     auto stage = [&](int kt, auto pf_tag, auto lt_tag) __attribute__((always_inline)) {
         constexpr bool pf = decltype(pf_tag)::value;
         constexpr int LT = decltype(lt_tag)::value;
         // stage kt has landed (and the scales issued with or before it)
-        if constexpr (pf) {
-            if (scaler) wait_vm<(C::ST - 2) * (C::L + 1)>();
-            else wait_vm<(C::ST - 2) * C::L>();
-        } else {
-            wait_vm<0>();
-        }
+        if constexpr (pf) wait_vm<(C::ST - 2) * (C::L + 1)>();
+        else wait_vm<0>();
         __syncthreads();
-        if constexpr (pf) issue_all(kt + C::ST - 1);
-        if constexpr (LT > 0) {
-            const char* sa = bt_lds + (kt % C::ST) * C::StageBytes;
-            const char* sb = sa + C::ABytes;
+        if constexpr (LT == 0) {
+            if constexpr (pf) issue(kt + C::ST - 1, 0, C::L + 1);
+        } else {
+            const char* st = bt_lds + (kt % C::ST) * C::StageBytes;
             const float* sc = reinterpret_cast<const float*>(bt_lds + C::ScaleOff + ((kt / 8) % 3) * C::SBuf) + kt % 8;
-            const float w0 = sw0[kt], w1 = sw1[kt];
-            float s[C::TM][LT];
+            uint4 wr[2][C::TM], tr[2][LT];  // codes of two steps
+            auto read = [&](int b, int c) __attribute__((always_inline)) {
+                const char* p = st + off[c];
 #pragma unroll
-            for (int j = 0; j < LT; ++j) {
-                const float tok = sc[trow[j] * 8];
-                s[0][j] = tok * w0;
-                s[1][j] = tok * w1;
-            }
-            f32x16 d[C::TM][LT];
+                for (int i = 0; i < C::TM; ++i) wr[b][i] = *reinterpret_cast<const uint4*>(p + wbase + i * kWStep);
 #pragma unroll
-            for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-                for (int j = 0; j < LT; ++j)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) d[i][j][v] = 0.0f;
-            auto chunk = [&](const char* base, int row, int c) {
-                return *reinterpret_cast<const uint4*>(base + row * 128 + (ring_swz(c, row) << 4));
+                for (int j = 0; j < LT; ++j) tr[b][j] = *reinterpret_cast<const uint4*>(p + tbase + j * 4096);
             };
+            read(0, 0);
+            read(1, 1);
+            const float w0 = sw0[kt], w1 = sw1[kt];
+            float tok[LT];
+#pragma unroll
+            for (int j = 0; j < LT; ++j) tok[j] = sc[trow[j] * 8];
+            __builtin_amdgcn_sched_barrier(0);
+            add_block(lt_tag);
+            constexpr int kPart = (C::L + 1 + 3) / 4;
+            const f32x16 zero = {};
             if constexpr (GATE) {
+                uint4 wf[2][C::TM][2], tf[2][LT][2];
+                auto cvt = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int i = 0; i < C::TM; ++i) cvt16(wr[b][i], wf[b][i]);
+#pragma unroll
+                    for (int j = 0; j < LT; ++j) cvt16(tr[b][j], tf[b][j]);
+                };
+                cvt(0);
+                read(0, 2);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint4 wf[C::TM][2], tf[LT][2];
-#pragma unroll
-                    for (int i = 0; i < C::TM; ++i) cvt16(chunk(sb, wrow[i], 2 * c + khalf), wf[i]);
-#pragma unroll
-                    for (int j = 0; j < LT; ++j) cvt16(chunk(sa, trow[j], 2 * c + khalf), tf[j]);
+                    const int b = c & 1;
+                    if constexpr (pf) issue(kt + C::ST - 1, c * kPart, (c + 1) * kPart);
+                    if (c < 3) cvt(b ^ 1);
+                    if (c == 0) read(1, 3);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < C::TM; ++i)
 #pragma unroll
                             for (int j = 0; j < LT; ++j)
-                                d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, wf[i][h]),
-                                                                                  __builtin_bit_cast(bf16x8, tf[j][h]),
-                                                                                  d[i][j], 0, 0, 0);
+                                d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                    __builtin_bit_cast(bf16x8, wf[b][i][h]), __builtin_bit_cast(bf16x8, tf[b][j][h]),
+                                    c == 0 && h == 0 ? zero : d[i][j], 0, 0, 0);
+#pragma unroll
+                    for (int q = 0; q < 2 * C::TM * LT; ++q) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // a product,
+                        __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);  // four conversions
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
+                auto cat = [](const uint4& x, const uint4& y) {
+                    return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+                };
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     i32x8 wf[C::TM], tf[LT];
-                    auto frag = [&](const char* base, int row) {
-                        const uint4 x = chunk(base, row, (2 * c + khalf) * 2), y = chunk(base, row, (2 * c + khalf) * 2 + 1);
-                        return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
-                    };
 #pragma unroll
-                    for (int i = 0; i < C::TM; ++i) wf[i] = frag(sb, wrow[i]);
+                    for (int i = 0; i < C::TM; ++i) wf[i] = cat(wr[0][i], wr[1][i]);
 #pragma unroll
-                    for (int j = 0; j < LT; ++j) tf[j] = frag(sa, trow[j]);
+                    for (int j = 0; j < LT; ++j) tf[j] = cat(tr[0][j], tr[1][j]);
+                    if (c == 0) {
+                        read(0, 2);
+                        read(1, 3);
+                    }
+                    if constexpr (pf) issue(kt + C::ST - 1, c * 2 * kPart, (c + 1) * 2 * kPart);
 #pragma unroll
                     for (int i = 0; i < C::TM; ++i)
 #pragma unroll
                         for (int j = 0; j < LT; ++j)
-                            d[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], tf[j], d[i][j], 0, 0, 0, 0, 0, 0);
+                            d[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], tf[j], c == 0 ? zero : d[i][j], 0,
+                                                                                      0, 0, 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-                for (int j = 0; j < LT; ++j)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[i][j][v] = __builtin_fmaf(d[i][j][v], s[i][j], acc[i][j][v]);
+            for (int j = 0; j < LT; ++j) {
+                sp[0][j] = tok[j] * w0;
+                sp[1][j] = tok[j] * w1;
+            }
         }
     };
     const int nmain = max(0, nk - (C::ST - 1));
     auto kloop = [&](auto lt_tag) __attribute__((always_inline)) {
         for (int kt = 0; kt < nmain; ++kt) stage(kt, std::true_type{}, lt_tag);
         for (int kt = nmain; kt < nk; ++kt) stage(kt, std::false_type{}, lt_tag);
+        add_block(lt_tag);
     };
     static_assert(C::TN <= 2, "live tile counts 0, 1 and 2");
     if (live == 0) kloop(std::integral_constant<int, 0>{});
@@ -358,18 +408,19 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
                         uint2{pack_bf2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
                               pack_bf2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
         __syncthreads();
-        for (int i = tid; i < C::BM * 32; i += C::Threads) {
-            const int r = i >> 5, n = n0 + 8 * (i & 31), p = ids_s[r];
+        constexpr int kVecs = C::BN / 8;  // 16-byte pieces of a row
+        for (int i = tid; i < C::BM * kVecs; i += C::Threads) {
+            const int r = i / kVecs, v = i % kVecs, n = n0 + 8 * v, p = ids_s[r];
             if (p < P && n < N)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.c) + (size_t)p * N + n) =
-                    *reinterpret_cast<const uint4*>(bt_lds + r * C::OutStride + 16 * (i & 31));
+                    *reinterpret_cast<const uint4*>(bt_lds + r * C::OutStride + 16 * v);
         }
     }
 }
 
 template <bool GATE, class C, bool NTW, bool FAR>
 static hipError_t launch_tile(const BlockArgs& a, int64_t cap, hipStream_t s) {
-    const int m_tiles = (int)(cap / C::BM), n_tiles = (a.N + 255) / 256;
+    const int m_tiles = (int)(cap / C::BM), n_tiles = (a.N + C::BN - 1) / C::BN;
     const int64_t nb = (int64_t)m_tiles * n_tiles;
     static const hipError_t attr =
         hipFuncSetAttribute(reinterpret_cast<const void*>(&block_tile_kernel<GATE, C, NTW, FAR>),
@@ -389,85 +440,131 @@ static hipError_t launch_tile_c(const BlockArgs& a, int64_t cap, bool far, hipSt
     return launch_tile<GATE, C, false, false>(a, cap, s);
 }
 
-// ------------------------------------------------------- float32 act (ring)
+// ------------------------------------------------------- float32 act (rows)
 //
-// Few rows per expert: blockIdx.y is an active expert, blockIdx.x a block of
-// 64 weight rows (GATE_UP: 32 gate rows and the matching up rows), blockIdx.z
-// a K split (DOWN).  The four wavefronts take the blocks of 128 k round robin
-// and reduce through LDS at the end; 16 token rows a pass.
+// Few rows per expert.  blockIdx.y is an active expert, blockIdx.x 64 of its
+// weight rows (GATE: 32 gate rows and the matching 32 up rows), blockIdx.z a K
+// split (DOWN).  The four wavefronts take the blocks of 128 k round robin,
+// weights straight from memory into the MFMA operands (16 rows x 64 bytes an
+// instruction, each byte read once: non-temporal), and reduce through LDS at the
+// end; 16 token rows a pass.  Four workgroups a CU keep 128 KB of weights in
+// flight; a second block's loads per wavefront cost the occupancy that does
+// this (128 experts at 16 tokens: gate/up 44 -> 57 us, down 33 -> 70).  Token rows are codes with scales (XDT MOE_FP8_E4M3),
+// or bfloat16 / float32 rows quantised here, block by block, as
+// moe_quant_block does: a lane holds 32 of a row's 128 values, the four lanes
+// of a row share their maximum.
 
-template <bool GATE>
-__global__ void __launch_bounds__(256) block_rows_kernel(BlockArgs g) {
+// One block of 128 k of a lane's token row: the raw values, then its codes
+// (bytes 16 lg .. and 64 + 16 lg .. of the block) and scale.
+template <int XDT>
+struct TokenBlock {
+    static constexpr int kVecs = XDT == MOE_F32 ? 8 : XDT == MOE_BF16 ? 4 : 2;
+    uint4 v[kVecs];
+    float s;
+    __device__ __forceinline__ void load(const void* a, const float* a_scale, size_t row, int K, int b, int lg) {
+        constexpr int kElem = XDT == MOE_F32 ? 4 : XDT == MOE_BF16 ? 2 : 1;
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a) + (row * K + 128 * (size_t)b + 16 * lg) * kElem);
+#pragma unroll
+        for (int u = 0; u < kVecs / 2; ++u) {
+            v[u] = p[u];
+            v[kVecs / 2 + u] = p[4 * kElem + u];  // 64 values on
+        }
+        if constexpr (XDT == MOE_FP8_E4M3) s = a_scale[row * (K / 128) + b];
+    }
+    __device__ __forceinline__ void codes(uint4& c0, uint4& c1, float& scale) const {
+        if constexpr (XDT == MOE_FP8_E4M3) {
+            c0 = v[0];
+            c1 = v[1];
+            scale = s;
+        } else {
+            float f[32];
+            unsigned m = 0;
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u) {
+                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (XDT == MOE_F32) {
+                        f[4 * u + i] = __uint_as_float(w[i]);
+                    } else {
+                        f[8 * u + 2 * i] = __uint_as_float(w[i] << 16);
+                        f[8 * u + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+            m = max(m, (unsigned)__shfl_xor((int)m, 16, 64));
+            m = max(m, (unsigned)__shfl_xor((int)m, 32, 64));
+            const BlockQuant bq(m);
+            c0 = uint4{bq.pack4(f[0], f[1], f[2], f[3]), bq.pack4(f[4], f[5], f[6], f[7]), bq.pack4(f[8], f[9], f[10], f[11]),
+                       bq.pack4(f[12], f[13], f[14], f[15])};
+            c1 = uint4{bq.pack4(f[16], f[17], f[18], f[19]), bq.pack4(f[20], f[21], f[22], f[23]),
+                       bq.pack4(f[24], f[25], f[26], f[27]), bq.pack4(f[28], f[29], f[30], f[31])};
+            scale = bq.scale;
+        }
+    }
+};
+
+template <bool GATE, int XDT>
+__global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
     const int slot = blockIdx.y;
-    if (slot >= *g.num_active) return;
-    const int e = g.active[slot];
-    const int cnt = g.counts[e], base = g.offsets[e];
+    int e, cnt, base = 0;
+    if (g.ids) {  // one token: pair `slot` is the only row of its expert
+        e = g.ids[slot];
+        cnt = 1;
+    } else {
+        e = g.active[slot];
+        if (e < 0) return;
+        cnt = g.counts[e];
+        base = g.offsets[e];
+    }
     __shared__ f32x4 red[4][4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
     const int N = g.N, K = g.K, I = N / 2, nkb = K / 128;
     const int kb0 = (int)((long)blockIdx.z * nkb / g.ksplit), kb1 = (int)((long)(blockIdx.z + 1) * nkb / g.ksplit);
     const int n0 = GATE ? blockIdx.x * 32 : blockIdx.x * 64;
-    const uint8_t* wexp = g.w + (size_t)e * N * K;
+    const uint8_t* wexp = g.w + (size_t)e * N * K + 16 * lg;
     const float* sexp = g.w_scale + (size_t)e * (N / 128) * nkb;
     const uint8_t* wrow[4];
-    const float* srow[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int row = GATE ? (t < 2 ? n0 + 16 * t : I + n0 + 16 * (t - 2)) : n0 + 16 * t;
         wrow[t] = wexp + (size_t)(row + lr) * K;
-        srow[t] = sexp + (size_t)(row / 128) * nkb;
     }
+    const float* s0 = sexp + (size_t)(n0 / 128) * nkb;
+    const float* s1 = GATE ? s0 + (size_t)(I / 128) * nkb : s0;
+
     for (int r0 = 0; r0 < cnt; r0 += 16) {
         const int r = r0 + lr;
-        const int p = g.sorted[base + min(r, cnt - 1)];
-        const int src = GATE ? p / g.topk : p;
+        const int p = g.ids ? slot : g.sorted[base + min(r, cnt - 1)];
+        const size_t src = GATE ? p / g.topk : p;
         f32x4 acc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int b = kb0 + wave; b < kb1; b += 4) {
-            const int k = 128 * b + 16 * lg;
-            uint4 b0, b1;
-            float s;
-            if constexpr (GATE) {
-                const uint8_t* arow = static_cast<const uint8_t*>(g.a) + (size_t)src * K + k;
-                b0 = *reinterpret_cast<const uint4*>(arow);
-                b1 = *reinterpret_cast<const uint4*>(arow + 64);
-                s = g.a_scale[(size_t)src * nkb + b];
-            } else {
-                const float4* arow = reinterpret_cast<const float4*>(static_cast<const float*>(g.a) + (size_t)src * K + k);
-                float4 v[8];
-                unsigned m = 0;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    v[u] = arow[u];
-                    v[4 + u] = arow[16 + u];
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    m = max(m, max(max(__float_as_uint(v[u].x) & 0x7fffffffu, __float_as_uint(v[u].y) & 0x7fffffffu),
-                                   max(__float_as_uint(v[u].z) & 0x7fffffffu, __float_as_uint(v[u].w) & 0x7fffffffu)));
-                m = max(m, (unsigned)__shfl_xor((int)m, 16, 64));
-                m = max(m, (unsigned)__shfl_xor((int)m, 32, 64));
-                const BlockQuant bq(m);
-                uint32_t q[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) q[u] = bq.pack4(v[u].x, v[u].y, v[u].z, v[u].w);
-                b0 = uint4{q[0], q[1], q[2], q[3]};
-                b1 = uint4{q[4], q[5], q[6], q[7]};
-                s = bq.scale;
-            }
+            uint4 w[4][2], c0, c1;
+            TokenBlock<XDT> x;
+            float sx;
+            x.load(g.a, g.a_scale, src, K, b, lg);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const uint4 a0 = *reinterpret_cast<const uint4*>(wrow[t] + k), a1 = *reinterpret_cast<const uint4*>(wrow[t] + k + 64);
+                w[t][0] = *reinterpret_cast<const uint4*>(wrow[t] + 128 * (size_t)b);
+                w[t][1] = *reinterpret_cast<const uint4*>(wrow[t] + 128 * (size_t)b + 64);
+            }
+            const float w0 = s0[b], w1 = s1[b];
+            x.codes(c0, c1, sx);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
                 f32x4 d = {0.f, 0.f, 0.f, 0.f};
                 if constexpr (GATE) {
-                    d = mfma_bf16_chunk(a0, b0, d);
-                    d = mfma_bf16_chunk(a1, b1, d);
+                    d = mfma_bf16_chunk(w[t][0], c0, d);
+                    d = mfma_bf16_chunk(w[t][1], c1, d);
                 } else {
-                    d = mfma_f8_16x16x128(a0, a1, b0, b1, d);
+                    d = mfma_f8_16x16x128(w[t][0], w[t][1], c0, c1, d);
                 }
-                const float sc = s * srow[t][b];
+                const float sc = sx * (t < 2 ? w0 : w1);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(d[v], sc, acc[t][v]);
             }
@@ -501,22 +598,43 @@ __global__ void __launch_bounds__(256) block_rows_kernel(BlockArgs g) {
 
 // ------------------------------------------------------------------ dispatch
 
+// Experts that M tokens reach under uniform routing.
+static double active_experts(int M, int E, int topk) { return E * (1.0 - __builtin_pow(1.0 - (double)topk / E, (double)M)); }
+
+// Rows per tile (alignment) from the rows per expert.  A tile streams its
+// weights once, so the tile should hold an expert's rows; a taller one keeps
+// more LDS per workgroup than it fills.  gate/up + down, us, 32 / 64 / 128 rows:
+// 8 experts of 4096 x 14336 at 16 rows an expert 223 / 230 / 282, at 24 285 / 240
+// / 290, at 48 350 / 264 / 316, at 64 447 / 389 / 365; 128 experts of 2048 x 768 at
+// 16 122 / 128 / 142, at 20 143 / 132 / 147, at 48 245 / 183 / 175.
 int block_tile_rows(int M, int E, int topk) {
     const long per_expert = (long)M * topk / E;
-    return per_expert > 48 ? 128 : per_expert > 16 ? 64 : 32;
+    return per_expert > 48 ? 128 : per_expert > 18 ? 64 : 32;
 }
 
 bool block_tile_rows_ok(int block_m) { return block_m == 32 || block_m == 64 || block_m == 128; }
 
-bool block_f32_act(int M, int E, int topk, int H, int I) { return M == 1; }
+// Whether a layer passes act in float32 (rows kernels).  They start their
+// weight stream at once and spread it over 64-row pieces; the tile kernels pay
+// for their ring and for whole 128-column blocks, which more than about two
+// rounds of workgroups or more rows per expert repay.  gate/up + down, us,
+// rows / tiles: 128 experts of 2048 x 768 at 16 tokens (492 workgroups) 69 / 85,
+// at 64 (756) 114 / 113; 8 of 4096 x 1024 at 8 rows an expert 26 / 41, at 16
+// 40 / 42; 64 of 4096 x 8192 at one token (512) 154 / 134, at 4 465 / 408.
+bool block_f32_act(int M, int E, int topk, int H, int I) {
+    (void)H;
+    return (long)M * topk <= 8L * E && (I / 128) * active_experts(M, E, topk) < 512.0;
+}
 
+// K splits of the float32-act down GEMM: about three workgroups a CU, each
+// split at least one block for every wavefront (one token of 8 experts of 4096 x
+// 14336: 48 us unsplit).
 int block_down_ksplit(int M, int topk, int E, int N, int K) {
     const long P = (long)M * topk;
     const long wgs = (long)(N / 64) * (P < E ? P : E);
-    if (wgs >= 256) return 1;
-    int ks = (int)((256 + wgs - 1) / wgs);
+    int ks = (int)((768 + wgs - 1) / wgs);
     if (ks > kMaxKsplit) ks = kMaxKsplit;
-    if (ks > K / 128 / 6) ks = K / 128 / 6;
+    if (ks > K / 128 / 4) ks = K / 128 / 4;  // a block for every wavefront of a split
     return ks < 1 ? 1 : ks;
 }
 
@@ -525,30 +643,42 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     const int P = c.M * c.topk;
     const BlockArgs a{c.a, c.a_scale, static_cast<const uint8_t*>(c.w), c.w_scale, c.al.sorted_ids, c.al.tile_expert,
                       c.al.expert_counts, c.al.expert_offsets, c.al.active_experts, c.al.num_active, c.topk, c.N, c.K,
-                      P, c.block_m, c.c, c.c_scale, c.ksplit, c.cpart, P <= 64L * c.E};
+                      P, c.block_m, c.c, c.c_scale, c.ksplit, c.cpart, c.ids, P <= 64L * c.E};
     const int slots = P < c.E ? P : c.E;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
     if (c.kind == MOE_GEMM_GATE_UP_SILU) {
-        hipLaunchKernelGGL((block_rows_kernel<true>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
+        if (c.x_bf16)
+            hipLaunchKernelGGL((block_rows_kernel<true, MOE_BF16>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((block_rows_kernel<true, MOE_FP8_E4M3>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     if (c.kind == MOE_GEMM_DOWN) {
-        hipLaunchKernelGGL((block_rows_kernel<false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((block_rows_kernel<false, MOE_F32>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     const bool gate = c.kind == MOE_GEMM_GATE_UP_SILU_E4M3;
     const bool far = (uint64_t)(gate ? c.M : P) * (uint64_t)c.K > 0xffffffffull;
-    using C32 = BtCfg<32, 1, 3>;
-    using C64 = BtCfg<64, 2, 3>;
-    using C128 = BtCfg<128, 2, 3>;
+    // Ring depth.  With about one workgroup a CU, only a deep ring keeps enough
+    // bytes in flight; with many, a shallow one lets two or more share a CU and
+    // hide each other's starts and ends.  us, deep / shallow: down of 8 experts of
+    // 4096 x 14336, 256 workgroups, 73 / 108; of 128 of 2048 x 768, 1300, 36 / 29;
+    // gate/up of 8 of 4096 x 1024, 64 workgroups, 30 / 44; of 128 of 2048 x 768, 756,
+    // 83 / 72.  (128-row tiles: the LDS holds one shape.)
+    const double wgs = active_experts(c.M, c.E, c.topk) * (gate ? c.N / 256 : (c.N + 127) / 128);
     if (gate) {
-        if (c.block_m == 32) return launch_tile_c<true, C32>(a, cap, far, s);
-        if (c.block_m == 64) return launch_tile_c<true, C64>(a, cap, far, s);
-        return launch_tile_c<true, C128>(a, cap, far, s);
+        if (c.block_m == 128) return launch_tile_c<true, BtCfg<128, 256, 2, 3>>(a, cap, far, s);
+        if (c.block_m == 64) return launch_tile_c<true, BtCfg<64, 256, 2, 3>>(a, cap, far, s);
+        if (wgs <= 256.0) return launch_tile_c<true, BtCfg<32, 256, 1, 4>>(a, cap, far, s);
+        return launch_tile_c<true, BtCfg<32, 256, 1, 2>>(a, cap, far, s);
     }
-    if (c.block_m == 32) return launch_tile_c<false, C32>(a, cap, far, s);
-    if (c.block_m == 64) return launch_tile_c<false, C64>(a, cap, far, s);
-    return launch_tile_c<false, C128>(a, cap, far, s);
+    if (c.block_m == 128) return launch_tile_c<false, BtCfg<128, 128, 4, 2>>(a, cap, far, s);
+    if (c.block_m == 64) {
+        if (wgs <= 512.0) return launch_tile_c<false, BtCfg<64, 128, 2, 4>>(a, cap, far, s);
+        return launch_tile_c<false, BtCfg<64, 128, 2, 3>>(a, cap, far, s);
+    }
+    if (wgs <= 512.0) return launch_tile_c<false, BtCfg<32, 128, 1, 4>>(a, cap, far, s);
+    return launch_tile_c<false, BtCfg<32, 128, 1, 3>>(a, cap, far, s);
 }
 
 }  // namespace moe

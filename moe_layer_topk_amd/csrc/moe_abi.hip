@@ -117,8 +117,8 @@ FusedLayout fused_layout(char* ws, moe_dtype dtype, int32_t M, int32_t E, int32_
     L.amax = c.take<float>(1);
     const bool blk = dtype == MOE_FP8_BLOCK;
     const bool codes = blk && !block_f32_act(M, E, topk, H, I);  // the GEMMs pass act as codes and scales
-    L.xq = blk ? c.take<char>((size_t)M * H) : nullptr;
-    L.xs = blk ? c.take<float>((size_t)M * (H / 128)) : nullptr;
+    L.xq = codes ? c.take<char>((size_t)M * H) : nullptr;
+    L.xs = codes ? c.take<float>((size_t)M * (H / 128)) : nullptr;
     L.act_s = codes ? c.take<float>((size_t)P * (I / 128)) : nullptr;
     L.act = c.take<char>((size_t)P * I * (codes ? 1 : act_bytes(dtype)));
     L.dc = down_combine_fits(dtype, M, topk, E, H, I, L.block_m);
@@ -350,14 +350,27 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
     const bool fp8 = dtype == MOE_FP8_E4M3;
     const moe_dtype inter = dtype == MOE_F32 ? MOE_F32 : MOE_BF16;
     if (dtype == MOE_FP8_BLOCK) {
-        const bool codes = L.act_s != nullptr;
-        if (launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess) return MOE_ERR_HIP;
-        const BlockGemmCall b1{codes ? MOE_GEMM_GATE_UP_SILU_E4M3 : MOE_GEMM_GATE_UP_SILU, L.xq, L.xs, w1, w1_scale,
-                               L.al, M, topk, E, 2 * I, H, L.block_m, L.act, L.act_s};
-        if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
-        const BlockGemmCall b2{codes ? MOE_GEMM_DOWN_E4M3_ACT : MOE_GEMM_DOWN, L.act, L.act_s, w2, w2_scale,
-                               L.al, M, topk, E, H, I, L.block_m, L.y, nullptr, L.ksplit, L.ypart};
-        if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
+        if (!L.act_s) {
+            // few rows per expert: x and act are quantised by the GEMMs that
+            // read them; one token needs no alignment (route_ids)
+            BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU, x, nullptr, w1, w1_scale, L.al, M, topk, E, 2 * I, H, L.block_m, L.act,
+                             nullptr};
+            b1.ids = route_ids;
+            b1.x_bf16 = true;
+            if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
+            BlockGemmCall b2{MOE_GEMM_DOWN, L.act, nullptr, w2, w2_scale, L.al, M, topk, E, H, I, L.block_m, L.y, nullptr,
+                             L.ksplit, L.ypart};
+            b2.ids = route_ids;
+            if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
+        } else {
+            if (launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess) return MOE_ERR_HIP;
+            const BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU_E4M3, L.xq, L.xs, w1, w1_scale, L.al, M, topk, E, 2 * I, H,
+                                   L.block_m, L.act, L.act_s};
+            if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
+            const BlockGemmCall b2{MOE_GEMM_DOWN_E4M3_ACT, L.act, L.act_s, w2, w2_scale, L.al, M, topk, E, H, I,
+                                   L.block_m, L.y, nullptr};
+            if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
+        }
         if (L.ksplit > 1) return hip_status(launch_combine_partials(L.ypart, L.ksplit, wts, M, topk, H, inter, out, s));
         return hip_status(launch_combine(inter, L.y, wts, M, topk, H, inter, out, s));
     }
@@ -420,6 +433,16 @@ moe_status run_fused(moe_dtype dtype, const void* x, const float* x_scale, const
     float* logits = const_cast<float*>(router_logits);
     // the activations' storage
     const moe_dtype xdt = (dtype == MOE_W4A16 || dtype == MOE_FP8_BLOCK) ? MOE_BF16 : dtype;
+    if (dtype == MOE_FP8_BLOCK && M == 1 && !L.act_s) {
+        // one token: its ids are all the alignment the GEMMs need
+        if (router_w && launch_router_logits(xdt, x, x_scale, router_w, M, E, H, logits, s) != hipSuccess)
+            return MOE_ERR_HIP;
+        const hipError_t st = route.spec ? launch_route_grouped(MOE_F32, logits, *route.spec, M, E, topk, ids, wts, s)
+                                         : launch_route(logits, M, E, topk, renormalize, ids, wts, s);
+        if (st != hipSuccess) return MOE_ERR_HIP;
+        return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s, nullptr,
+                           renormalize, ids);
+    }
     if (route.spec) {
         if (launch_route_grouped(MOE_F32, logits, *route.spec, M, E, topk, ids, wts, s) != hipSuccess ||
             launch_align(ids, M, topk, E, L.block_m, L.cap, L.al, fp8 ? L.amax : nullptr, s) != hipSuccess)
