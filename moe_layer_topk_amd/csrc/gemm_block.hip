@@ -446,73 +446,68 @@ static hipError_t launch_tile_c(const BlockArgs& a, int64_t cap, bool far, hipSt
 // weight rows (GATE: 32 gate rows and the matching 32 up rows), blockIdx.z a K
 // split (DOWN).  The four wavefronts take the blocks of 128 k round robin,
 // weights straight from memory into the MFMA operands (16 rows x 64 bytes an
-// instruction, each byte read once: non-temporal), and reduce through LDS at the
-// end; 16 token rows a pass.  Four workgroups a CU keep 128 KB of weights in
-// flight; a second block's loads per wavefront cost the occupancy that does
-// this (128 experts at 16 tokens: gate/up 44 -> 57 us, down 33 -> 70).  Token rows are codes with scales (XDT MOE_FP8_E4M3),
-// or bfloat16 / float32 rows quantised here, block by block, as
-// moe_quant_block does: a lane holds 32 of a row's 128 values, the four lanes
-// of a row share their maximum.
+// instruction), and reduce through LDS at the end; 16 token rows a pass.  DOWN
+// quantises its float32 rows block by block as moe_quant_block does: a lane
+// holds 32 of a row's 128 values, the four lanes of a row share their maximum.
+//
+// What keeps bytes in flight is workgroups: loading a second block ahead in each
+// wavefront costs the occupancy (128 experts of 2048 x 768 at 16 tokens: gate/up
+// 40 -> 57 us, down 29 -> 70), and the non-temporal hint makes the two 64-byte
+// halves of a line two fetches (40 -> 54, 29 -> 34).
 
-// One block of 128 k of a lane's token row: the raw values, then its codes
-// (bytes 16 lg .. and 64 + 16 lg .. of the block) and scale.
-template <int XDT>
+// One block of 128 k of a lane's token row: its values as loaded, then its
+// codes (bytes 16 lg .. and 64 + 16 lg .. of the block) and scale.
+template <bool F32>
 struct TokenBlock {
-    static constexpr int kVecs = XDT == MOE_F32 ? 8 : XDT == MOE_BF16 ? 4 : 2;
+    static constexpr int kVecs = F32 ? 8 : 2;
     uint4 v[kVecs];
     float s;
     __device__ __forceinline__ void load(const void* a, const float* a_scale, size_t row, int K, int b, int lg) {
-        constexpr int kElem = XDT == MOE_F32 ? 4 : XDT == MOE_BF16 ? 2 : 1;
+        constexpr int kElem = F32 ? 4 : 1;
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a) + (row * K + 128 * (size_t)b + 16 * lg) * kElem);
 #pragma unroll
         for (int u = 0; u < kVecs / 2; ++u) {
             v[u] = p[u];
             v[kVecs / 2 + u] = p[4 * kElem + u];  // 64 values on
         }
-        if constexpr (XDT == MOE_FP8_E4M3) s = a_scale[row * (K / 128) + b];
+        if constexpr (!F32) s = a_scale[row * (K / 128) + b];
     }
     __device__ __forceinline__ void codes(uint4& c0, uint4& c1, float& scale) const {
-        if constexpr (XDT == MOE_FP8_E4M3) {
+        if constexpr (!F32) {
             c0 = v[0];
             c1 = v[1];
             scale = s;
         } else {
-            float f[32];
             unsigned m = 0;
 #pragma unroll
-            for (int u = 0; u < kVecs; ++u) {
-                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (XDT == MOE_F32) {
-                        f[4 * u + i] = __uint_as_float(w[i]);
-                    } else {
-                        f[8 * u + 2 * i] = __uint_as_float(w[i] << 16);
-                        f[8 * u + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+            for (int u = 0; u < 8; ++u)
+                m = max(m, max(max(v[u].x & 0x7fffffffu, v[u].y & 0x7fffffffu), max(v[u].z & 0x7fffffffu, v[u].w & 0x7fffffffu)));
             m = max(m, (unsigned)__shfl_xor((int)m, 16, 64));
             m = max(m, (unsigned)__shfl_xor((int)m, 32, 64));
             const BlockQuant bq(m);
-            c0 = uint4{bq.pack4(f[0], f[1], f[2], f[3]), bq.pack4(f[4], f[5], f[6], f[7]), bq.pack4(f[8], f[9], f[10], f[11]),
-                       bq.pack4(f[12], f[13], f[14], f[15])};
-            c1 = uint4{bq.pack4(f[16], f[17], f[18], f[19]), bq.pack4(f[20], f[21], f[22], f[23]),
-                       bq.pack4(f[24], f[25], f[26], f[27]), bq.pack4(f[28], f[29], f[30], f[31])};
+            auto pack = [&](const uint4& w) {
+                return bq.pack4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            };
+            c0 = uint4{pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3])};
+            c1 = uint4{pack(v[4]), pack(v[5]), pack(v[6]), pack(v[7])};
             scale = bq.scale;
         }
     }
 };
 
-template <bool GATE, int XDT>
+// ONE: a single token.  Its topk ids give the experts (no alignment is read),
+// and a wavefront quantises the row's blocks it will multiply (bfloat16 x for
+// GATE, float32 act for DOWN) into its own LDS, 16 blocks at a time, 8 values a
+// lane: what every lane group of the MFMA reads is then one broadcast.
+template <bool GATE, bool ONE>
 __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
+    constexpr int kChunk = 16;  // blocks a wavefront quantises at a time
     const int slot = blockIdx.y;
-    int e, cnt, base = 0;
-    if (g.ids) {  // one token: pair `slot` is the only row of its expert
+    int e, cnt, base;
+    if constexpr (ONE) {
         e = g.ids[slot];
         cnt = 1;
+        base = 0;
     } else {
         e = g.active[slot];
         if (e < 0) return;
@@ -520,6 +515,8 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
         base = g.offsets[e];
     }
     __shared__ f32x4 red[4][4][64];
+    __shared__ __attribute__((aligned(16))) uint8_t one_q[ONE ? 4 : 1][ONE ? kChunk * 128 : 16];
+    __shared__ float one_s[ONE ? 4 : 1][kChunk];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
     const int N = g.N, K = g.K, I = N / 2, nkb = K / 128;
@@ -538,23 +535,50 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
 
     for (int r0 = 0; r0 < cnt; r0 += 16) {
         const int r = r0 + lr;
-        const int p = g.ids ? slot : g.sorted[base + min(r, cnt - 1)];
+        const int p = ONE ? slot : g.sorted[base + min(r, cnt - 1)];
         const size_t src = GATE ? p / g.topk : p;
         f32x4 acc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int b = kb0 + wave; b < kb1; b += 4) {
+        // the wavefront's i-th block is kb0 + wave + 4 i
+        const int mine = kb1 - kb0 > wave ? (kb1 - kb0 - wave + 3) / 4 : 0;
+        auto quantise = [&](int i0) __attribute__((always_inline)) {
+            for (int i = i0; i < min(i0 + kChunk, mine); i += 4) {
+                const int ib = i + (lane >> 4), l = lane & 15;
+                const int b = kb0 + wave + 4 * min(ib, mine - 1);
+                float v[8];
+                load8<GATE ? MOE_BF16 : MOE_F32>(g.a, src * K + 128 * (size_t)b + 8 * l, v);
+                const BlockQuant bq(row16_max_u32(amax8(v)));
+                const uint2 q = {bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
+                if (ib < mine) {
+                    *reinterpret_cast<uint2*>(&one_q[wave][(ib - i0) * 128 + 8 * l]) = q;
+                    if (l == 0) one_s[wave][ib - i0] = bq.scale;
+                }
+            }
+            // (read by this wavefront alone, after its own writes)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        };
+        for (int i = 0; i < mine; ++i) {
+            const int b = kb0 + wave + 4 * i;
             uint4 w[4][2], c0, c1;
-            TokenBlock<XDT> x;
+            TokenBlock<!GATE> x;
             float sx;
-            x.load(g.a, g.a_scale, src, K, b, lg);
+            if constexpr (!ONE) x.load(g.a, g.a_scale, src, K, b, lg);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 w[t][0] = *reinterpret_cast<const uint4*>(wrow[t] + 128 * (size_t)b);
                 w[t][1] = *reinterpret_cast<const uint4*>(wrow[t] + 128 * (size_t)b + 64);
             }
             const float w0 = s0[b], w1 = s1[b];
-            x.codes(c0, c1, sx);
+            if constexpr (ONE) {
+                if (i % kChunk == 0) quantise(i);
+                const uint8_t* q = &one_q[wave][(i % kChunk) * 128 + 16 * lg];
+                c0 = *reinterpret_cast<const uint4*>(q);
+                c1 = *reinterpret_cast<const uint4*>(q + 64);
+                sx = one_s[wave][i % kChunk];
+            } else {
+                x.codes(c0, c1, sx);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 f32x4 d = {0.f, 0.f, 0.f, 0.f};
@@ -647,14 +671,13 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     const int slots = P < c.E ? P : c.E;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
     if (c.kind == MOE_GEMM_GATE_UP_SILU) {
-        if (c.x_bf16)
-            hipLaunchKernelGGL((block_rows_kernel<true, MOE_BF16>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
-        else
-            hipLaunchKernelGGL((block_rows_kernel<true, MOE_FP8_E4M3>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
+        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<true, true>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((block_rows_kernel<true, false>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     if (c.kind == MOE_GEMM_DOWN) {
-        hipLaunchKernelGGL((block_rows_kernel<false, MOE_F32>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
+        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<false, true>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     const bool gate = c.kind == MOE_GEMM_GATE_UP_SILU_E4M3;

@@ -117,19 +117,21 @@ FusedLayout fused_layout(char* ws, moe_dtype dtype, int32_t M, int32_t E, int32_
     L.amax = c.take<float>(1);
     const bool blk = dtype == MOE_FP8_BLOCK;
     const bool codes = blk && !block_f32_act(M, E, topk, H, I);  // the GEMMs pass act as codes and scales
-    L.xq = codes ? c.take<char>((size_t)M * H) : nullptr;
-    L.xs = codes ? c.take<float>((size_t)M * (H / 128)) : nullptr;
+    L.xq = blk ? c.take<char>((size_t)M * H) : nullptr;
+    L.xs = blk ? c.take<float>((size_t)M * (H / 128)) : nullptr;
     L.act_s = codes ? c.take<float>((size_t)P * (I / 128)) : nullptr;
     L.act = c.take<char>((size_t)P * I * (codes ? 1 : act_bytes(dtype)));
+    // (block layers with float32 act: y as float32 partials, split or not)
+    const bool f32_y = blk && !codes;
     L.dc = down_combine_fits(dtype, M, topk, E, H, I, L.block_m);
-    L.y = L.dc ? nullptr : c.take<char>((size_t)P * H * inter_bytes(dtype));
+    L.y = (L.dc || f32_y) ? nullptr : c.take<char>((size_t)P * H * inter_bytes(dtype));
     L.q_on_load = dtype == MOE_FP8_E4M3 && fp8_down_quantises_on_load(M, topk, E, H, I, L.block_m);
     L.act_q = (dtype == MOE_FP8_E4M3 && !L.q_on_load) ? c.take<char>((size_t)P * I) : nullptr;
     if (blk)
         L.ksplit = codes ? 1 : block_down_ksplit(M, topk, E, H, I);
     else
         L.ksplit = L.dc ? 1 : down_ksplit(dtype, M, topk, E, H, I, L.block_m);
-    L.ypart = L.ksplit > 1 ? c.take<float>((size_t)L.ksplit * P * H) : nullptr;
+    L.ypart = (L.ksplit > 1 || f32_y) ? c.take<float>((size_t)L.ksplit * P * H) : nullptr;
     // one e4m3 token (the GEMMs may route it themselves): the intermediate's
     // amax as partials, one per 32 gate/up output columns of each slot
     L.amax_nparts = (dtype == MOE_FP8_E4M3 && M == 1) ? (P < E ? (int32_t)P : E) * (I / 32) : 0;
@@ -350,20 +352,18 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
     const bool fp8 = dtype == MOE_FP8_E4M3;
     const moe_dtype inter = dtype == MOE_F32 ? MOE_F32 : MOE_BF16;
     if (dtype == MOE_FP8_BLOCK) {
+        // (one token whose ids are all the GEMMs need quantises x there)
+        if (!route_ids && launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess) return MOE_ERR_HIP;
         if (!L.act_s) {
-            // few rows per expert: x and act are quantised by the GEMMs that
-            // read them; one token needs no alignment (route_ids)
-            BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU, x, nullptr, w1, w1_scale, L.al, M, topk, E, 2 * I, H, L.block_m, L.act,
-                             nullptr};
+            BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU, route_ids ? x : L.xq, L.xs, w1, w1_scale, L.al, M, topk, E, 2 * I, H,
+                             L.block_m, L.act, nullptr};
             b1.ids = route_ids;
-            b1.x_bf16 = true;
             if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
             BlockGemmCall b2{MOE_GEMM_DOWN, L.act, nullptr, w2, w2_scale, L.al, M, topk, E, H, I, L.block_m, L.y, nullptr,
                              L.ksplit, L.ypart};
             b2.ids = route_ids;
             if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
         } else {
-            if (launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess) return MOE_ERR_HIP;
             const BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU_E4M3, L.xq, L.xs, w1, w1_scale, L.al, M, topk, E, 2 * I, H,
                                    L.block_m, L.act, L.act_s};
             if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
@@ -371,7 +371,7 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
                                    L.block_m, L.y, nullptr};
             if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
         }
-        if (L.ksplit > 1) return hip_status(launch_combine_partials(L.ypart, L.ksplit, wts, M, topk, H, inter, out, s));
+        if (L.ypart) return hip_status(launch_combine_partials(L.ypart, L.ksplit, wts, M, topk, H, inter, out, s));
         return hip_status(launch_combine(inter, L.y, wts, M, topk, H, inter, out, s));
     }
     GemmCall g1{MOE_GEMM_GATE_UP_SILU, dtype, x, x_scale, w1, w1_scale, L.al, M, topk, E, 2 * I, H,

@@ -2,6 +2,7 @@
 // shared by moe_quant_block and the grouped GEMMs.
 #pragma once
 
+#include "moe.h"
 #include "moe_device.h"
 #include "moe_tile.h"
 
@@ -15,6 +16,32 @@ __device__ __forceinline__ unsigned row16_max_u32(unsigned x) {
     x = max(x, (unsigned)__builtin_amdgcn_update_dpp((int)x, (int)x, 0x141, 0xF, 0xF, false));  // row_half_mirror
     x = max(x, (unsigned)__builtin_amdgcn_update_dpp((int)x, (int)x, 0x140, 0xF, 0xF, false));  // row_mirror
     return x;
+}
+
+// Eight consecutive values of x as float32; i a multiple of 8.
+template <int XDT>
+__device__ __forceinline__ void load8(const void* x, size_t i, float (&v)[8]) {
+    if constexpr (XDT == MOE_F32) {
+        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ unsigned amax8(const float (&v)[8]) {
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    return m;
 }
 
 constexpr float kMinBlockScale = 1.17549435e-38f;  // 2^-126

@@ -129,8 +129,9 @@ struct BlockGemmCall {
     float* c_scale;          // GATE_UP_SILU_E4M3: scales of the codes c
     int ksplit = 1;          // DOWN over float32 act: split of K across workgroups
     float* cpart = nullptr;  // with ksplit > 1: float32 partials [ksplit][P][N] instead of c
-    const int32_t* ids = nullptr;  // float32-act kinds, one token: its topk ids instead of the alignment
-    bool x_bf16 = false;           // GATE_UP_SILU: a is bfloat16 rows, quantised on load (a_scale unused)
+    // float32-act kinds, one token: its topk ids, read instead of the alignment;
+    // GATE_UP_SILU then takes a as the bfloat16 row and quantises it itself
+    const int32_t* ids = nullptr;
 };
 hipError_t launch_block_gemm(const BlockGemmCall& g, hipStream_t s);
 

@@ -360,7 +360,8 @@ __device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, i
         m = wave_max_f32(m);
     }
     int sel = 0;
-    if (!route_choose<float, V>(r, E, topk, l, rb, m, sel)) route_choose<double, V>(r, E, topk, l, rb, m, sel);
+    if (__builtin_expect(!route_choose<float, V>(r, E, topk, l, rb, m, sel), 0))
+        route_choose<double, V>(r, E, topk, l, rb, m, sel);
 
     // the chosen experts' scores, from their logits
     float lj = 0.0f;

@@ -5,32 +5,6 @@
 
 namespace moe {
 
-// Eight consecutive values of x as float32 bits; i a multiple of 8.
-template <int XDT>
-__device__ __forceinline__ void load8(const void* x, size_t i, float (&v)[8]) {
-    if constexpr (XDT == MOE_F32) {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-    }
-}
-
-__device__ __forceinline__ unsigned amax8(const float (&v)[8]) {
-    unsigned m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    return m;
-}
-
 // One scale per 128 values of a row: 16 lanes hold a block, 8 values each.
 template <int XDT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const void* __restrict__ x, size_t nblk,

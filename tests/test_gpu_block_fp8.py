@@ -273,7 +273,10 @@ def test_layer(dev, M, E, k, H, I):
 
 @pytest.mark.parametrize("M", [16, 100, 300])
 def test_layer_is_its_stages(dev, M):
-    """The fused layer and the same steps through their own entry points."""
+    """The fused layer and the same steps through their own entry points: the
+    same bits, except that a small batch keeps y in float32 where the stage
+    rounds it to bfloat16 (half a step, 2^-8, of every weighted y, and half a
+    step of the output, whose own rounding may fall the other way)."""
     import moe_layer_topk_amd as moe
     E, k, H, I = 16, 4, 384, 256
     x, lg, b, _, (dx, dlg, dw1, ds1, dw2, ds2) = layer_inputs(M, E, k, H, I, dev)
@@ -285,7 +288,10 @@ def test_layer_is_its_stages(dev, M):
     a, as_ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP_SILU_E4M3, q, dw1, al, M, k, a_scale=qs, w_scale=ds1)
     y, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_DOWN_E4M3_ACT, a, dw2, al, M, k, a_scale=as_, w_scale=ds2)
     want = moe.moe_combine(y, wts, k)
-    assert torch.equal(out, want)
+    if M >= 100:
+        assert torch.equal(out, want)
+    half = (y.float().abs().view(M, k, H) * wts[:, :, None]).sum(1).double() * 2.0 ** -8
+    within((out.double() - want.double()).abs().cpu(), (half + (want.double().abs() + half) * 2.0 ** -7).cpu())
 
 
 @pytest.mark.parametrize("name", ["f32", "bf16", "fp8", "w4a16"])
