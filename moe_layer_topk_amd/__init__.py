@@ -17,7 +17,6 @@ hidden states.  moe_route_grouped / fused_moe_grouped route with a Routing
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -76,25 +75,29 @@ def _layer_dtype(w: torch.Tensor, w_scale) -> int:
     return moe_dtype(w)
 
 
-def _on(t: torch.Tensor):
-    """The context in which t's device is the current one (the library launches on it)."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+def _call(fn, what: str, dev, *args) -> None:
+    """fn(*args) with dev the current device (the library launches on it)."""
+    if dev.index == torch.cuda.current_device():
+        check(fn(*args), what)
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args), what)
 
 
 def _need(name: str, t, dtypes, shape, device) -> None:
     """A contiguous tensor of one of the dtypes, of this shape, on this device."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+            and t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is missing")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is not contiguous")
 
 
 _F32, _F8 = (torch.float32,), (torch.float8_e4m3fn,)
@@ -143,9 +146,8 @@ def moe_route_grouped(logits: torch.Tensor, topk: int, routing: Routing, topk_id
         topk_weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
     _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
     _need("topk_weights", topk_weights, _F32, (M, topk), dev)
-    with _on(logits):
-        check(lib().moe_route_grouped(_DTYPES[logits.dtype], _p(logits), routing._ref, M, E, topk, _p(topk_ids),
-                                      _p(topk_weights), stream), "moe_route_grouped")
+    _call(lib().moe_route_grouped, "moe_route_grouped", dev, _DTYPES[logits.dtype], logits.data_ptr(), routing._ref, M, E,
+          topk, topk_ids.data_ptr(), topk_weights.data_ptr(), stream)
     return topk_ids, topk_weights
 
 
@@ -238,9 +240,8 @@ def _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_scale):
             c_scale = torch.empty((P, cols // 128), dtype=torch.float32, device=dev)
         _need("c_amax (the scales of c)", c_scale, _F32, (P, cols // 128), dev)
     bufs = align_struct(al)
-    with _on(w):
-        check(lib().moe_grouped_gemm(kind, MOE_FP8_BLOCK, _p(a), _p(a_scale), _p(w), _p(w_scale), ctypes.byref(bufs),
-                                     M, topk, E, N, K, al["block_m"], _p(c), _p(c_scale), stream), "moe_grouped_gemm")
+    _call(lib().moe_grouped_gemm, "moe_grouped_gemm", dev, kind, MOE_FP8_BLOCK, _p(a), _p(a_scale), _p(w), _p(w_scale),
+          ctypes.byref(bufs), M, topk, E, N, K, al["block_m"], _p(c), _p(c_scale), stream)
     return c, c_scale
 
 
@@ -261,9 +262,8 @@ def moe_quant_block(x: torch.Tensor, block_rows: int = 1, q=None, scale=None):
         scale = torch.empty(shape, dtype=torch.float32, device=dev)
     _need("q", q, _CODES, (rows, K), dev)
     _need("scale", scale, _F32, shape, dev)
-    with _on(x):
-        check(lib().moe_quant_block(_DTYPES[x.dtype], _p(x), rows, K, block_rows, _p(q), _p(scale), stream),
-              "moe_quant_block")
+    _call(lib().moe_quant_block, "moe_quant_block", dev, _DTYPES[x.dtype], x.data_ptr(), rows, K, block_rows, q.data_ptr(),
+          scale.data_ptr(), stream)
     return q, scale
 
 
@@ -331,11 +331,9 @@ def fused_moe_grouped(x, router_logits, w1, w2, topk: int, routing: Routing, x_s
         _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
     if topk_weights is not None:
         _need("topk_weights", topk_weights, _F32, (M, topk), dev)
-    with _on(x):
-        check(lib().fused_moe_grouped(dt, _p(x), _p(x_scale), _p(router_logits), routing._ref, _p(w1), _p(w1_scale),
-                                      _p(w2), _p(w2_scale), M, E, topk, H, I, _p(out), _p(topk_ids),
-                                      _p(topk_weights), _p(workspace), workspace.numel(), stream),
-              "fused_moe_grouped")
+    _call(lib().fused_moe_grouped, "fused_moe_grouped", dev, dt, _p(x), _p(x_scale), _p(router_logits), routing._ref,
+          _p(w1), _p(w1_scale), _p(w2), _p(w2_scale), M, E, topk, H, I, _p(out), _p(topk_ids), _p(topk_weights),
+          _p(workspace), workspace.numel(), stream)
     return out
 
 

@@ -498,9 +498,15 @@ struct TokenBlock {
 // ONE: a single token.  Its topk ids give the experts (no alignment is read),
 // and a wavefront quantises the row's blocks it will multiply (bfloat16 x for
 // GATE, float32 act for DOWN) into its own LDS, 16 blocks at a time, 8 values a
-// lane: what every lane group of the MFMA reads is then one broadcast.
+// lane: what every lane group of the MFMA reads is then one broadcast.  Eight
+// wavefronts share a workgroup's blocks (one token leaves the chip half empty,
+// and a wavefront's blocks run one after another).
+template <bool ONE>
+constexpr int kRowsWaves = ONE ? 8 : 4;
+
 template <bool GATE, bool ONE>
-__global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
+__global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(BlockArgs g) {
+    constexpr int W = kRowsWaves<ONE>;
     constexpr int kChunk = 16;  // blocks a wavefront quantises at a time
     const int slot = blockIdx.y;
     int e, cnt, base;
@@ -514,9 +520,9 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
         cnt = g.counts[e];
         base = g.offsets[e];
     }
-    __shared__ f32x4 red[4][4][64];
-    __shared__ __attribute__((aligned(16))) uint8_t one_q[ONE ? 4 : 1][ONE ? kChunk * 128 : 16];
-    __shared__ float one_s[ONE ? 4 : 1][kChunk];
+    __shared__ f32x4 red[W][4][64];
+    __shared__ __attribute__((aligned(16))) uint8_t one_q[ONE ? W : 1][ONE ? kChunk * 128 : 16];
+    __shared__ float one_s[ONE ? W : 1][kChunk];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
     const int N = g.N, K = g.K, I = N / 2, nkb = K / 128;
@@ -540,12 +546,12 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
         f32x4 acc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // the wavefront's i-th block is kb0 + wave + 4 i
-        const int mine = kb1 - kb0 > wave ? (kb1 - kb0 - wave + 3) / 4 : 0;
+        // the wavefront's i-th block is kb0 + wave + W i
+        const int mine = kb1 - kb0 > wave ? (kb1 - kb0 - wave + W - 1) / W : 0;
         auto quantise = [&](int i0) __attribute__((always_inline)) {
             for (int i = i0; i < min(i0 + kChunk, mine); i += 4) {
                 const int ib = i + (lane >> 4), l = lane & 15;
-                const int b = kb0 + wave + 4 * min(ib, mine - 1);
+                const int b = kb0 + wave + W * min(ib, mine - 1);
                 float v[8];
                 load8<GATE ? MOE_BF16 : MOE_F32>(g.a, src * K + 128 * (size_t)b + 8 * l, v);
                 const BlockQuant bq(row16_max_u32(amax8(v)));
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         };
         for (int i = 0; i < mine; ++i) {
-            const int b = kb0 + wave + 4 * i;
+            const int b = kb0 + wave + W * i;
             uint4 w[4][2], c0, c1;
             TokenBlock<!GATE> x;
             float sx;
@@ -598,7 +604,12 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
         for (int t = 0; t < 4; ++t) red[wave][t][lane] = acc[t];
         __syncthreads();
         if (r < cnt) {
-            auto sum = [&](int t) { return red[0][t][lane] + red[1][t][lane] + red[2][t][lane] + red[3][t][lane]; };
+            auto sum = [&](int t) {
+                f32x4 v = red[0][t][lane];
+#pragma unroll
+                for (int u = 1; u < W; ++u) v += red[u][t][lane];
+                return v;
+            };
             if constexpr (GATE) {
                 if (wave < 2) {
                     const f32x4 gs = sum(wave), us = sum(wave + 2);
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(256, 2) block_rows_kernel(BlockArgs g) {
                     for (int v = 0; v < 4; ++v) o[v] = silu(gs[v]) * us[v];
                     *reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + (size_t)p * I + n0 + 16 * wave + 4 * lg) = o;
                 }
-            } else {
+            } else if (wave < 4) {
                 const f32x4 y = sum(wave);
                 const int n = n0 + 16 * wave + 4 * lg;
                 if (g.cpart)
@@ -671,12 +682,12 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     const int slots = P < c.E ? P : c.E;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
     if (c.kind == MOE_GEMM_GATE_UP_SILU) {
-        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<true, true>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
+        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<true, true>), dim3(c.N / 64, slots, 1), dim3(64 * kRowsWaves<true>), 0, s, a);
         else hipLaunchKernelGGL((block_rows_kernel<true, false>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     if (c.kind == MOE_GEMM_DOWN) {
-        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<false, true>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
+        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<false, true>), dim3(c.N / 64, slots, c.ksplit), dim3(64 * kRowsWaves<true>), 0, s, a);
         else hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
         return hipGetLastError();
     }

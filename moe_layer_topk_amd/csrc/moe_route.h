@@ -34,6 +34,8 @@ struct RankKey<float> {
     __device__ static __forceinline__ key of(float v) { return order_key(v); }
     __device__ static __forceinline__ key wave_max(key k) { return wave_max_u32(k); }
     __device__ static __forceinline__ float value(key k) { return key_value(k); }
+    __device__ static __forceinline__ key max2(key a, key b) { return a > b ? a : b; }
+    __device__ static __forceinline__ key min2(key a, key b) { return a < b ? a : b; }
 };
 template <>
 struct RankKey<double> {
@@ -53,6 +55,8 @@ struct RankKey<double> {
     __device__ static __forceinline__ double value(key k) {
         return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
     }
+    __device__ static __forceinline__ key max2(key a, key b) { return a > b ? a : b; }
+    __device__ static __forceinline__ key min2(key a, key b) { return a < b ? a : b; }
 };
 
 // v of the lane whose number differs in bit `step` from this one's.  Steps 0
@@ -68,7 +72,13 @@ __device__ __forceinline__ float lane_swap(float v, int step) {
         default: return __shfl_xor(v, 1 << step, 64);
     }
 }
+__device__ __forceinline__ unsigned lane_swap(unsigned v, int step) {
+    return __float_as_uint(lane_swap(__uint_as_float(v), step));
+}
 __device__ __forceinline__ double lane_swap(double v, int step) { return __shfl_xor(v, 1 << step, 64); }
+__device__ __forceinline__ unsigned long long lane_swap(unsigned long long v, int step) {
+    return (unsigned long long)__shfl_xor((long long)v, 1 << step, 64);
+}
 
 __device__ __forceinline__ float lane_read(float v, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
@@ -135,42 +145,63 @@ __device__ __forceinline__ void load_logits(const void* logits, bool bf16, size_
     for (int q = 0; q < V; ++q) l[q] = l[q] == l[q] ? l[q] : ninf;
 }
 
-// What a wavefront keeps over its tokens: the biases of its experts.
-template <int V>
-struct RouteBias {
+// Groups of a router: none, whole lanes (a power of two of lanes each, so the
+// two best of a group merge by lane swaps), or any size (one masked maximum per
+// group and place).
+enum { kNoGroups = 0, kLaneGroups = 1, kAnyGroups = 2 };
+
+inline int group_mode(const RouteSpec& r, int E, int V) {
+    if (r.topk_groups >= r.n_groups) return kNoGroups;
+    const int gs = E / r.n_groups, lanes = gs / V;
+    return gs % V == 0 && (lanes & (lanes - 1)) == 0 ? kLaneGroups : kAnyGroups;
+}
+
+// What a wavefront keeps over its tokens: the biases of its experts, where its
+// group's score lies.
+template <int V, int GM, bool BIASED>
+struct RouteWave {
     float b[V];
-    float top;  // largest |bias|
-    __device__ __forceinline__ void load(const RouteSpec& r, int E) {
-        const int e0 = V * (int)__lane_id();
-        float m = 0.0f;
+    float top;    // largest |bias|
+    int stride;   // lanes from one group's score to the next
+    int g0;       // this lane's group (GM kAnyGroups: lane g holds group g)
+    int gq[V];    // lane holding the score of the group of candidate q
+    __device__ __forceinline__ RouteWave(const RouteSpec& r, int E) {
+        const int lane = __lane_id(), e0 = V * lane;
+        top = 0.0f;
+        if constexpr (BIASED) {
+            float m = 0.0f;
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            b[q] = (r.bias && e0 + q < E) ? r.bias[e0 + q] : 0.0f;
-            m = fmaxf(m, fabsf(b[q]));
+            for (int q = 0; q < V; ++q) {
+                b[q] = e0 + q < E ? r.bias[e0 + q] : 0.0f;
+                m = fmaxf(m, fabsf(b[q]));
+            }
+            top = wave_max_f32(m);
         }
-        top = r.bias ? wave_max_f32(m) : 0.0f;
+        if constexpr (GM != kNoGroups) {
+            const int gs = E / r.n_groups;
+            stride = GM == kLaneGroups ? gs / V : 1;
+            g0 = lane / stride;
+#pragma unroll
+            for (int q = 0; q < V; ++q) gq[q] = min((e0 + q) / gs, r.n_groups - 1) * stride;
+        }
     }
 };
 
-// One pass in T.  Returns false (float only) if a choice was too close to
-// call; else lane j < topk holds the j-th expert in sel.
-template <typename T, int V>
+// One pass in T: lane j < topk ends with the j-th expert in sel.  False (float
+// only) if a choice was too close to call.
+template <typename T, int V, int GM, bool BIASED>
 __device__ __forceinline__ bool route_choose(const RouteSpec& r, int E, int topk, const float (&l)[V],
-                                             const RouteBias<V>& rb, float m, int& sel) {
+                                             const RouteWave<V, GM, BIASED>& rw, float m, int& sel) {
     using RK = RankKey<T>;
     using key = typename RK::key;
+    constexpr bool f32 = sizeof(T) == 4;
     const int lane = __lane_id();
     const int e0 = V * lane;
     const T ninf = -(T)__builtin_inff();
-    constexpr bool f32 = sizeof(T) == 4;
-    const bool grouped = r.topk_groups < r.n_groups;
-    const bool biased = r.bias != nullptr;
 
     T c[V];  // choices
     float eta = 0.0f;
-#pragma unroll
-    for (int q = 0; q < V; ++q) c[q] = (T)l[q];
-    if (grouped || biased) {
+    if constexpr (GM != kNoGroups || BIASED) {
         if (r.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
             for (int q = 0; q < V; ++q) {
@@ -197,48 +228,41 @@ __device__ __forceinline__ bool route_choose(const RouteSpec& r, int E, int topk
             }
             eta = 1.90734863e-06f * (float)inv;  // 2^-19 of the largest
         }
-        if (biased) {
+        if constexpr (BIASED) {
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                c[q] += (T)rb.b[q];
+                c[q] += (T)rw.b[q];
                 c[q] = c[q] == c[q] ? c[q] : ninf;
             }
-            eta += 5.96046448e-08f * (1.0f + rb.top);
+            eta += 5.96046448e-08f * (1.0f + rw.top);
         }
     }
 
-    bool live[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) live[q] = e0 + q < E;
     bool close = false;
-    if (grouped) {
-        const int gs = E / r.n_groups;
-        const int lpg = gs / V;  // lanes of a group, if groups are whole lanes
-        const bool whole = gs % V == 0 && (lpg & (lpg - 1)) == 0;
+    uint64_t kept = ~0ull;
+    if constexpr (GM != kNoGroups) {
         T mine;  // lane g * stride: the score of group g
-        int stride;
-        if (whole) {
-            T a = ninf, b = ninf;  // the two best of the lane, then of the group
+        if constexpr (GM == kLaneGroups) {
+            key a = 0, b = 0;  // the two best of the lane, then of the group
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const T lo = a < c[q] ? a : c[q];
-                a = a < c[q] ? c[q] : a;
-                b = b < lo ? lo : b;
+                const key x = RK::of(c[q]);
+                b = RK::max2(b, RK::min2(a, x));
+                a = RK::max2(a, x);
             }
+            const int lanes = __builtin_amdgcn_readfirstlane(rw.stride);
 #pragma unroll
             for (int step = 0; step < 6; ++step) {
-                if ((1 << step) < lpg) {
-                    const T oa = lane_swap(a, step), ob = lane_swap(b, step);
-                    const T lo = a < oa ? a : oa, hb = b < ob ? ob : b;
-                    a = a < oa ? oa : a;
-                    b = lo < hb ? hb : lo;
-                }
+                if ((1 << step) >= lanes) break;
+                const key oa = lane_swap(a, step), ob = lane_swap(b, step);
+                b = RK::max2(RK::min2(a, oa), RK::max2(b, ob));
+                a = RK::max2(a, oa);
             }
-            mine = r.group_top == 2 ? a + b : a;
-            stride = lpg;
+            // (a lane group of one expert has no second: group_top is 1 then)
+            mine = r.group_top == 2 ? RK::value(a) + RK::value(b) : RK::value(a);
         } else {
             mine = ninf;
-            stride = 1;
+            const int gs = E / r.n_groups;
             for (int g = 0; g < r.n_groups; ++g) {
                 key k[V];
                 key best = 0;
@@ -269,75 +293,81 @@ __device__ __forceinline__ bool route_choose(const RouteSpec& r, int E, int topk
             }
         }
         mine = mine == mine ? mine : ninf;
-        const int g0 = lane / stride;  // this lane's group (lanes past the last: ignored)
-        int rank = 0;
+        // rank among the groups; in float32 an equal score counts as too close
+        int rank = 0, near = 0;
+        const float tol = 8.0f * eta + 4.76837158e-07f * (float)fabs((double)mine);
+        const int stride = __builtin_amdgcn_readfirstlane(rw.stride);
+#pragma unroll 8
         for (int g = 0; g < r.n_groups; ++g) {
             const T o = lane_read(mine, g * stride);
-            rank += (o > mine || (o == mine && g < g0)) ? 1 : 0;
             if constexpr (f32) {
-                const float d = fabsf(o - mine);
-                close |= g != g0 && !(d > 8.0f * eta + 2.38418579e-07f * fabsf(o));
+                rank += o > mine ? 1 : 0;
+                near += fabsf(o - mine) > tol ? 0 : 1;  // (itself too)
+            } else {
+                rank += (o > mine || (o == mine && g < rw.g0)) ? 1 : 0;
             }
         }
-        const bool group_lane = lane < r.n_groups * stride;
-        close = close && group_lane;
-        const uint64_t kept = __ballot(group_lane && rank < r.topk_groups);
-#pragma unroll
-        for (int q = 0; q < V; ++q) live[q] = live[q] && ((kept >> (((e0 + q) / gs) * stride)) & 1);
+        const bool group_lane = lane < r.n_groups * rw.stride;
+        close = f32 && group_lane && near > 1;
+        kept = __ballot(group_lane && rank < r.topk_groups);
     }
 
-    // the lane's candidates, best first, equal ones in index order (dead: key 0)
+    // the lane's candidates, best first, equal ones in index order (no candidate: key 0)
     key k[V];
     int idx[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-        k[q] = live[q] ? RK::of(biased ? c[q] : (T)l[q]) : 0;
+        bool live = e0 + q < E;
+        if constexpr (GM != kNoGroups) live = live && ((kept >> rw.gq[q]) & 1);
+        const key of = RK::of(BIASED ? c[q] : (T)l[q]);
+        k[q] = live ? of : 0;
         idx[q] = e0 + q;
     }
-    auto order = [&](int x, int y) __attribute__((always_inline)) {
-        const bool sw = k[y] > k[x] || (k[y] == k[x] && idx[y] < idx[x]);
-        const key tk = sw ? k[x] : k[y];
-        const int ti = sw ? idx[x] : idx[y];
-        k[x] = sw ? k[y] : k[x];
-        idx[x] = sw ? idx[y] : idx[x];
-        k[y] = tk;
-        idx[y] = ti;
-    };
-    if constexpr (V == 2) order(0, 1);
-    if constexpr (V == 4) {
-        order(0, 1);
-        order(2, 3);
-        order(0, 2);
-        order(1, 3);
-        order(1, 2);
-    }
-    const float tol = 4.0f * eta;
-    T last = 0;
+    // neighbours change places only if the later one is larger: stable
+#pragma unroll
+    for (int pass = 0; pass < V; ++pass)
+#pragma unroll
+        for (int x = pass & 1; x + 1 < V; x += 2) {
+            const bool sw = k[x + 1] > k[x];
+            const key hi = RK::max2(k[x], k[x + 1]), lo = RK::min2(k[x], k[x + 1]);
+            const int ih = sw ? idx[x + 1] : idx[x], il = sw ? idx[x] : idx[x + 1];
+            k[x] = hi;
+            k[x + 1] = lo;
+            idx[x] = ih;
+            idx[x + 1] = il;
+        }
+    // take the best head of the 64 lists, topk times
+    key taken = 0;
     for (int j = 0; j < topk; ++j) {
         const key best = RK::wave_max(k[0]);
         const int at = (int)__builtin_ctzll(__ballot(k[0] == best));
         const int e = __builtin_amdgcn_readlane(idx[0], at);
-        if (lane == j) sel = e;
-        if constexpr (f32) {
-            if (biased) {
-                const T v = RK::value(best);
-                close |= j > 0 && !(last - v > tol);
-                last = v;
-            }
-        }
-        if (lane == at) {
+        const bool slot = lane == j, pop = lane == at;
+        sel = slot ? e : sel;
+        taken = slot ? best : taken;
+        key kn[V];
+        int in[V];
 #pragma unroll
-            for (int q = 0; q + 1 < V; ++q) {
-                k[q] = k[q + 1];
-                idx[q] = idx[q + 1];
-            }
-            k[V - 1] = 0;
+        for (int q = 0; q + 1 < V; ++q) {
+            kn[q] = k[q + 1];
+            in[q] = idx[q + 1];
+        }
+        kn[V - 1] = 0;
+        in[V - 1] = idx[V - 1];
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            k[q] = pop ? kn[q] : k[q];
+            idx[q] = pop ? in[q] : idx[q];
         }
     }
     if constexpr (f32) {
-        if (biased) {
-            const key best = RK::wave_max(k[0]);  // the best one left out
-            close |= best != 0 && !(last - RK::value(best) > tol);
+        if constexpr (BIASED) {
+            // neighbours among the taken, and the best one left out (none: key 0)
+            const key left = RK::wave_max(k[0]);
+            key next = (key)__shfl_down((int)taken, 1, 64);
+            next = lane == topk - 1 ? left : next;
+            const float d = RK::value(taken) - RK::value(next);
+            close = close || (lane < topk && next != 0 && !(d > 4.0f * eta));
         }
         return __ballot(close) == 0;
     }
@@ -346,9 +376,9 @@ __device__ __forceinline__ bool route_choose(const RouteSpec& r, int E, int topk
 
 // Routes the token whose logits are l: lane j < topk ends with expert *sel and
 // weight *w.
-template <int V>
+template <int V, int GM, bool BIASED>
 __device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, int topk, const float (&l)[V],
-                                                    const RouteBias<V>& rb, int* sel_out, float* w_out) {
+                                                    const RouteWave<V, GM, BIASED>& rw, int* sel_out, float* w_out) {
     const int lane = __lane_id();
     const float ninf = -__builtin_inff();
     const bool soft = r.score == MOE_SCORE_SOFTMAX;
@@ -360,8 +390,8 @@ __device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, i
         m = wave_max_f32(m);
     }
     int sel = 0;
-    if (__builtin_expect(!route_choose<float, V>(r, E, topk, l, rb, m, sel), 0))
-        route_choose<double, V>(r, E, topk, l, rb, m, sel);
+    if (__builtin_expect(!route_choose<float, V, GM, BIASED>(r, E, topk, l, rw, m, sel), 0))
+        route_choose<double, V, GM, BIASED>(r, E, topk, l, rw, m, sel);
 
     // the chosen experts' scores, from their logits
     float lj = 0.0f;
