@@ -283,11 +283,13 @@ moe_status fused_moe_cached(moe_expert_cache* c, const void* x, const float* x_s
     // expert ids renamed to slots; the layer runs over the C slots
     for (int64_t p = 0; p < P; ++p) host_ids[p] = c->slot_of[host_ids[p]];
     if (hipMemcpyAsync(L.remap, host_ids, (size_t)P * 4, hipMemcpyHostToDevice, s) != hipSuccess) return MOE_ERR_HIP;
-    if (launch_align(L.remap, M, topk, C, L.block_m, L.cap, L.al, c->dtype == MOE_FP8_E4M3 ? L.amax : nullptr, s) !=
-        hipSuccess)
+    // (one token of a block fp8 layer: its ids are all the GEMMs need)
+    const bool one = c->dtype == MOE_FP8_BLOCK && M == 1 && !L.act_s;
+    if (!one && launch_align(L.remap, M, topk, C, L.block_m, L.cap, L.al, c->dtype == MOE_FP8_E4M3 ? L.amax : nullptr,
+                             s) != hipSuccess)
         return MOE_ERR_HIP;
     st = run_experts(c->dtype, x, x_scale, c->slots.w1, c->slots.w1_scale, c->slots.w2, c->slots.w2_scale, M, C, topk,
-                     H, I, out, wts, L, s);
+                     H, I, out, wts, L, s, nullptr, renormalize, one ? L.remap : nullptr);
     if (st != MOE_OK) return st;
     for (int32_t e : need) c->slot_call[c->slot_of[e]] = c->ncall;
     if (hipEventRecord(c->call_ev[c->ncall % kRing], s) != hipSuccess) return MOE_ERR_HIP;

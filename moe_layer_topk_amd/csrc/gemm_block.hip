@@ -495,10 +495,10 @@ struct TokenBlock {
     }
 };
 
-// ONE: a single token.  Its topk ids give the experts (no alignment is read),
-// and a wavefront quantises the row's blocks it will multiply (bfloat16 x for
-// GATE, float32 act for DOWN) into its own LDS, 16 blocks at a time, 8 values a
-// lane: what every lane group of the MFMA reads is then one broadcast.  Eight
+// ONE (GATE): a single token.  Its topk ids give the experts (no alignment is
+// read), and a wavefront quantises the blocks of the bfloat16 row that it will
+// multiply into its own LDS, 16 blocks at a time, 8 values a lane: what every
+// lane group of the MFMA reads is then one broadcast.  Eight
 // wavefronts share a workgroup's blocks (one token leaves the chip half empty,
 // and a wavefront's blocks run one after another).
 template <bool ONE>
@@ -507,6 +507,7 @@ constexpr int kRowsWaves = ONE ? 8 : 4;
 template <bool GATE, bool ONE>
 __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(BlockArgs g) {
     constexpr int W = kRowsWaves<ONE>;
+    static_assert(GATE || !ONE, "one token's down GEMM is block_down_one_kernel");
     constexpr int kChunk = 16;  // blocks a wavefront quantises at a time
     const int slot = blockIdx.y;
     int e, cnt, base;
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(Blo
                 const int ib = i + (lane >> 4), l = lane & 15;
                 const int b = kb0 + wave + W * min(ib, mine - 1);
                 float v[8];
-                load8<GATE ? MOE_BF16 : MOE_F32>(g.a, src * K + 128 * (size_t)b + 8 * l, v);
+                load8<MOE_BF16>(g.a, src * K + 128 * (size_t)b + 8 * l, v);
                 const BlockQuant bq(row16_max_u32(amax8(v)));
                 const uint2 q = {bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
                 if (ib < mine) {
@@ -631,6 +632,104 @@ __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(Blo
     }
 }
 
+// ------------------------------------------------- one token, down + combine
+//
+// A workgroup owns 16 columns of the output for all of the token's experts, so
+// their weighted sum needs no other workgroup and no launch of its own:
+// wavefront u takes unit u = (expert slot, K split), the units' columns meet in
+// LDS, and out = sum over slots ascending of weight * y, y the sum of its splits
+// ascending.  act [topk][K] float32 is quantised by the wavefront that
+// multiplies it.  128 experts of 2048 x 768, top 8: 128 workgroups; 8 of 4096 x
+// 14336, top 2: 256, four splits each.
+constexpr int kOneWaves = 8, kOneUnits = 16;  // units: topk * max(1, 8 / topk) <= 16
+
+__global__ void __launch_bounds__(64 * kOneWaves, 2) block_down_one_kernel(BlockArgs g, const float* __restrict__ wts,
+                                                                        uint16_t* __restrict__ out) {
+    constexpr int kChunk = 16;
+    __shared__ __attribute__((aligned(16))) uint8_t one_q[kOneWaves][kChunk * 128];
+    __shared__ float one_s[kOneWaves][kChunk];
+    __shared__ float part[kOneUnits][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int N = g.N, K = g.K, nkb = K / 128, n0 = blockIdx.x * 16;
+    const int ks = max(1, kOneWaves / g.topk), units = g.topk * ks;
+    for (int u = wave; u < units; u += kOneWaves) {
+        const int slot = u / ks, z = u - slot * ks;
+        const int e = g.ids[slot];
+        const int kb0 = (int)((long)z * nkb / ks), nb = (int)((long)(z + 1) * nkb / ks) - kb0;
+        const uint8_t* wrow = g.w + ((size_t)e * N + n0 + lr) * K + 128 * (size_t)kb0 + 16 * lg;
+        const float* srow = g.w_scale + ((size_t)e * (N / 128) + n0 / 128) * nkb + kb0;
+        const float* arow = static_cast<const float*>(g.a) + (size_t)slot * K + 128 * (size_t)kb0;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int c0 = 0; c0 < nb; c0 += kChunk) {
+            const int cn = min(kChunk, nb - c0);
+            // the first blocks' weights are on their way while act is quantised
+            constexpr int U = 4;
+            uint4 w[U][2];
+            auto load = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    const uint8_t* p = wrow + 128 * (size_t)(c0 + min(i + q, cn - 1));
+                    w[q][0] = *reinterpret_cast<const uint4*>(p);
+                    w[q][1] = *reinterpret_cast<const uint4*>(p + 64);
+                }
+            };
+            load(0);
+            for (int i = 0; i < cn; i += 4) {
+                const int ib = i + (lane >> 4), l = lane & 15;
+                float v[8];
+                load8<MOE_F32>(arow, 128 * (size_t)(c0 + min(ib, cn - 1)) + 8 * l, v);
+                const BlockQuant bq(row16_max_u32(amax8(v)));
+                if (ib < cn) {
+                    *reinterpret_cast<uint2*>(&one_q[wave][ib * 128 + 8 * l]) =
+                        uint2{bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
+                    if (l == 0) one_s[wave][ib] = bq.scale;
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            for (int i = 0; i < cn; i += U) {
+                if (i > 0) load(i);
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    if (i + q >= cn) break;
+                    const uint8_t* t = &one_q[wave][(i + q) * 128 + 16 * lg];
+                    const f32x4 d = mfma_f8_16x16x128(w[q][0], w[q][1], *reinterpret_cast<const uint4*>(t),
+                                                      *reinterpret_cast<const uint4*>(t + 64), f32x4{0.f, 0.f, 0.f, 0.f});
+                    const float sc = one_s[wave][i + q] * srow[c0 + i + q];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(d[v], sc, acc[v]);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the codes are read before the next chunk's
+        }
+        if (lr == 0) *reinterpret_cast<f32x4*>(&part[u][4 * lg]) = acc;
+    }
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        float o = 0.0f;
+        for (int j = 0; j < g.topk; ++j) {
+            float y = part[j * ks][threadIdx.x];
+            for (int z = 1; z < ks; ++z) y += part[j * ks + z][threadIdx.x];
+            o = __builtin_fmaf(wts[j], y, o);
+        }
+        out[n0 + threadIdx.x] = f2bf(o);
+    }
+}
+
+hipError_t launch_block_down_one(const BlockGemmCall& c, const float* wts, void* out, hipStream_t s) {
+    static_assert(kMaxTopk <= kOneUnits, "a unit for every slot");
+    BlockArgs a{};
+    a.a = c.a;
+    a.w = static_cast<const uint8_t*>(c.w);
+    a.w_scale = c.w_scale;
+    a.topk = c.topk;
+    a.N = c.N;
+    a.K = c.K;
+    a.ids = c.ids;
+    hipLaunchKernelGGL(block_down_one_kernel, dim3(c.N / 16), dim3(64 * kOneWaves), 0, s, a, wts, static_cast<uint16_t*>(out));
+    return hipGetLastError();
+}
+
 // ------------------------------------------------------------------ dispatch
 
 // Experts that M tokens reach under uniform routing.
@@ -687,8 +786,7 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
         return hipGetLastError();
     }
     if (c.kind == MOE_GEMM_DOWN) {
-        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<false, true>), dim3(c.N / 64, slots, c.ksplit), dim3(64 * kRowsWaves<true>), 0, s, a);
-        else hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     const bool gate = c.kind == MOE_GEMM_GATE_UP_SILU_E4M3;

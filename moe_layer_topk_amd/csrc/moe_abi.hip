@@ -362,6 +362,7 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
             BlockGemmCall b2{MOE_GEMM_DOWN, L.act, nullptr, w2, w2_scale, L.al, M, topk, E, H, I, L.block_m, L.y, nullptr,
                              L.ksplit, L.ypart};
             b2.ids = route_ids;
+            if (route_ids) return hip_status(launch_block_down_one(b2, wts, out, s));  // y stays on chip
             if (launch_block_gemm(b2, s) != hipSuccess) return MOE_ERR_HIP;
         } else {
             const BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU_E4M3, L.xq, L.xs, w1, w1_scale, L.al, M, topk, E, 2 * I, H,

@@ -135,6 +135,10 @@ struct BlockGemmCall {
 };
 hipError_t launch_block_gemm(const BlockGemmCall& g, hipStream_t s);
 
+// One token's DOWN over float32 act with the combine: out [N] bfloat16 from
+// the topk ids c.ids and weights wts (c.c, c.al and the scales of a are unused).
+hipError_t launch_block_down_one(const BlockGemmCall& c, const float* wts, void* out, hipStream_t s);
+
 // MOE_FP8_BLOCK layers: tile height, whether the GEMMs pass the intermediate
 // in float32 (ring kernels), and then the K split of the down GEMM.
 int block_tile_rows(int M, int E, int topk);
