@@ -262,7 +262,11 @@ moe_status fused_moe_cached(moe_expert_cache* c, const void* x, const float* x_s
         hipStreamWaitEvent(s, c->call_ev[(c->ncall - 1) % kRing], 0) != hipSuccess)
         return MOE_ERR_HIP;
     // route over the E experts, then the ids to the host
-    if (launch_route(router_logits, M, E, topk, renormalize, ids, wts, s) != hipSuccess) return MOE_ERR_HIP;
+    const hipError_t routed =
+        c->dtype == MOE_FP8_BLOCK
+            ? launch_route_grouped(MOE_F32, router_logits, softmax_spec(renormalize), M, E, topk, ids, wts, s)
+            : launch_route(router_logits, M, E, topk, renormalize, ids, wts, s);
+    if (routed != hipSuccess) return MOE_ERR_HIP;
     if (hipMemcpyAsync(host_ids, ids, (size_t)P * 4, hipMemcpyDeviceToHost, s) != hipSuccess ||
         hipStreamSynchronize(s) != hipSuccess)
         return MOE_ERR_HIP;

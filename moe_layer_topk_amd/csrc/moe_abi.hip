@@ -47,6 +47,8 @@ static RouteSpec route_spec(const moe_routing& r) {
     return RouteSpec{(int)r.score, r.bias, r.n_groups, r.topk_groups, r.group_top, r.renormalize, r.scale};
 }
 
+RouteSpec softmax_spec(int32_t renormalize) { return RouteSpec{MOE_SCORE_SOFTMAX, nullptr, 1, 1, 1, renormalize, 1.0f}; }
+
 bool known_dtype(moe_dtype d) {
     return d == MOE_F32 || d == MOE_BF16 || d == MOE_FP8_E4M3 || d == MOE_W4A16 || d == MOE_FP8_BLOCK;
 }
@@ -348,12 +350,13 @@ moe_status check_fused(moe_dtype dtype, const void* x, const float* x_scale, con
 moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, const void* w1, const float* w1_scale,
                        const void* w2, const float* w2_scale, int32_t M, int32_t E, int32_t topk, int32_t H,
                        int32_t I, void* out, const float* wts, const FusedLayout& L, hipStream_t s,
-                       const float* route_logits, int32_t renormalize, int32_t* route_ids) {
+                       const float* route_logits, int32_t renormalize, int32_t* route_ids, bool x_quantised) {
     const bool fp8 = dtype == MOE_FP8_E4M3;
     const moe_dtype inter = dtype == MOE_F32 ? MOE_F32 : MOE_BF16;
     if (dtype == MOE_FP8_BLOCK) {
         // (one token whose ids are all the GEMMs need quantises x there)
-        if (!route_ids && launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess) return MOE_ERR_HIP;
+        if (!route_ids && !x_quantised && launch_quant_block(MOE_BF16, x, M, H, 1, L.xq, L.xs, s) != hipSuccess)
+            return MOE_ERR_HIP;
         if (!L.act_s) {
             BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU, route_ids ? x : L.xq, L.xs, w1, w1_scale, L.al, M, topk, E, 2 * I, H,
                              L.block_m, L.act, nullptr};
@@ -434,21 +437,30 @@ moe_status run_fused(moe_dtype dtype, const void* x, const float* x_scale, const
     float* logits = const_cast<float*>(router_logits);
     // the activations' storage
     const moe_dtype xdt = (dtype == MOE_W4A16 || dtype == MOE_FP8_BLOCK) ? MOE_BF16 : dtype;
-    if (dtype == MOE_FP8_BLOCK && M == 1 && !L.act_s) {
-        // one token: its ids are all the alignment the GEMMs need
+    const bool blk = dtype == MOE_FP8_BLOCK;
+    if (blk || route.spec) {
+        const RouteSpec spec = route.spec ? *route.spec : softmax_spec(renormalize);
         if (router_w && launch_router_logits(xdt, x, x_scale, router_w, M, E, H, logits, s) != hipSuccess)
             return MOE_ERR_HIP;
-        const hipError_t st = route.spec ? launch_route_grouped(MOE_F32, logits, *route.spec, M, E, topk, ids, wts, s)
-                                         : launch_route(logits, M, E, topk, renormalize, ids, wts, s);
-        if (st != hipSuccess) return MOE_ERR_HIP;
-        return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s, nullptr,
-                           renormalize, ids);
-    }
-    if (route.spec) {
-        if (launch_route_grouped(MOE_F32, logits, *route.spec, M, E, topk, ids, wts, s) != hipSuccess ||
-            launch_align(ids, M, topk, E, L.block_m, L.cap, L.al, fp8 ? L.amax : nullptr, s) != hipSuccess)
+        if (blk && M == 1 && !L.act_s) {
+            // one token: its ids are all the alignment the GEMMs need
+            if (launch_route_grouped(MOE_F32, logits, spec, M, E, topk, ids, wts, s) != hipSuccess) return MOE_ERR_HIP;
+            return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s, nullptr,
+                               renormalize, ids);
+        }
+        // block fp8: the routing launch quantises x beside it
+        void* xq = blk ? L.xq : nullptr;
+        float* amax = fp8 ? L.amax : nullptr;
+        if (route_align_fits(M)) {
+            if (launch_route_grouped_align(logits, spec, M, E, topk, ids, wts, L.block_m, L.cap, L.al, amax, s, x, H, xq,
+                                           L.xs) != hipSuccess)
+                return MOE_ERR_HIP;
+        } else if (launch_route_grouped(MOE_F32, logits, spec, M, E, topk, ids, wts, s, x, H, xq, L.xs) != hipSuccess ||
+                   launch_align(ids, M, topk, E, L.block_m, L.cap, L.al, amax, s) != hipSuccess) {
             return MOE_ERR_HIP;
-        return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s);
+        }
+        return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s, nullptr,
+                           renormalize, nullptr, blk);
     }
     if (self_route_fits(dtype, M, E, topk, H, I, L)) {
         // one token on the decode kernels: they route it themselves, so the

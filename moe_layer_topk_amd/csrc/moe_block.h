@@ -80,4 +80,28 @@ struct BlockQuant {
     }
 };
 
+// Rows to quantise beside other work of a launch (q NULL: none).
+struct QuantJob {
+    const uint16_t* x;  // bfloat16
+    size_t nblk;        // blocks of 128 values
+    uint8_t* q;
+    float* scale;
+};
+
+// Blocks of 128 values of x by `nthreads` threads of workgroup `blk` of `nblks`:
+// 16 lanes hold a block, 8 values each.
+template <int XDT>
+__device__ __forceinline__ void quant_rows(const void* x, size_t nblk, uint8_t* q, float* scale, int blk, int nblks,
+                                           int nthreads) {
+    const int l = threadIdx.x & 15, per = nthreads / 16;
+    for (size_t b = (size_t)blk * per + (threadIdx.x >> 4); b < nblk; b += (size_t)nblks * per) {
+        float v[8];
+        load8<XDT>(x, b * 128 + 8 * l, v);
+        const BlockQuant bq(row16_max_u32(amax8(v)));
+        *reinterpret_cast<uint2*>(q + b * 128 + 8 * l) =
+            uint2{bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
+        if (l == 0) scale[b] = bq.scale;
+    }
+}
+
 }  // namespace moe

@@ -60,11 +60,15 @@ moe_status check_fused(moe_dtype dtype, const void* x, const float* x_scale, con
                        int32_t E, int32_t topk, int32_t H, int32_t I, const void* out, const int32_t* topk_ids_out,
                        const float* topk_weights_out);
 
+// The plain softmax router (no bias, no groups).
+RouteSpec softmax_spec(int32_t renormalize);
+
 // GATE_UP -> DOWN -> combine, once L.al aligns the pairs over the E experts
 // that w1/w2 hold and wts holds the routing weights.
 moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, const void* w1, const float* w1_scale,
                        const void* w2, const float* w2_scale, int32_t M, int32_t E, int32_t topk, int32_t H,
                        int32_t I, void* out, const float* wts, const FusedLayout& L, hipStream_t s,
-                       const float* route_logits = nullptr, int32_t renormalize = 1, int32_t* route_ids = nullptr);
+                       const float* route_logits = nullptr, int32_t renormalize = 1, int32_t* route_ids = nullptr,
+                       bool x_quantised = false);
 
 }  // namespace moe

@@ -31,8 +31,16 @@ struct RouteSpec {
     int n_groups, topk_groups, group_top, renormalize;
     float scale;
 };
+// xq non-null: the launch also quantises x [M][H] (bfloat16) to codes xq and
+// scales xs, as launch_quant_block does.
 hipError_t launch_route_grouped(moe_dtype ldt, const void* logits, const RouteSpec& r, int M, int E, int topk,
-                                int32_t* ids, float* weights, hipStream_t s);
+                                int32_t* ids, float* weights, hipStream_t s, const void* x = nullptr, int H = 0,
+                                void* xq = nullptr, float* xs = nullptr);
+// The same with the alignment, for M <= 16 (route_align_fits).
+hipError_t launch_route_grouped_align(const float* logits, const RouteSpec& r, int M, int E, int topk, int32_t* ids,
+                                      float* weights, int block_m, int64_t cap, const moe_align_bufs& out,
+                                      float* zero_f32, hipStream_t s, const void* x = nullptr, int H = 0,
+                                      void* xq = nullptr, float* xs = nullptr);
 
 // Both steps in one launch for M <= 16 (one wavefront routes each token).
 bool route_align_fits(int M);

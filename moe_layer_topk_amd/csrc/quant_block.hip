@@ -9,15 +9,7 @@ namespace moe {
 template <int XDT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const void* __restrict__ x, size_t nblk,
                                                          uint8_t* __restrict__ q, float* __restrict__ scale) {
-    const int l = threadIdx.x & 15;
-    for (size_t b = (size_t)blockIdx.x * 16 + (threadIdx.x >> 4); b < nblk; b += (size_t)gridDim.x * 16) {
-        float v[8];
-        load8<XDT>(x, b * 128 + 8 * l, v);
-        const BlockQuant bq(row16_max_u32(amax8(v)));
-        *reinterpret_cast<uint2*>(q + b * 128 + 8 * l) =
-            uint2{bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
-        if (l == 0) scale[b] = bq.scale;
-    }
+    quant_rows<XDT>(x, nblk, q, scale, blockIdx.x, gridDim.x, 256);
 }
 
 // One scale per 128 x 128 block: a workgroup per block, thread (r, l) holds 8
