@@ -180,6 +180,7 @@ def moe_align(topk_ids: torch.Tensor, E: int, block_m: int) -> dict:
         "active_experts": torch.empty(max(min(E, M * topk), 1), **i32),
         "num_active": torch.empty(1, **i32),
         "block_m": block_m,
+        "pairs": M * topk,
     }
     check(lib().moe_align(_p(topk_ids), M, topk, E, block_m, align_struct(out), _stream(topk_ids)), "moe_align")
     return out
@@ -239,9 +240,12 @@ def _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_scale):
         if c_scale is None:
             c_scale = torch.empty((P, cols // 128), dtype=torch.float32, device=dev)
         _need("c_amax (the scales of c)", c_scale, _F32, (P, cols // 128), dev)
+    block_m = al["block_m"]
+    if al["pairs"] != P or al["expert_counts"].numel() != E or al["sorted_ids"].device != dev:
+        raise ValueError("the alignment (moe_align) is of another batch, number of experts or device")
     bufs = align_struct(al)
     _call(lib().moe_grouped_gemm, "moe_grouped_gemm", dev, kind, MOE_FP8_BLOCK, _p(a), _p(a_scale), _p(w), _p(w_scale),
-          ctypes.byref(bufs), M, topk, E, N, K, al["block_m"], _p(c), _p(c_scale), stream)
+          ctypes.byref(bufs), M, topk, E, N, K, block_m, _p(c), _p(c_scale), stream)
     return c, c_scale
 
 
@@ -296,15 +300,35 @@ def fused_moe_workspace_size(dtype: int, M: int, E: int, topk: int, H: int, I: i
     return lib().fused_moe_workspace_size(dtype, M, E, topk, H, I)
 
 
-def _check_block_layer(x, w1, w2, w1_scale, w2_scale) -> None:
-    """Operands of a layer on block-scaled e4m3 weights."""
+def _check_block_weights(w1, w2, w1_scale, w2_scale, dev) -> None:
+    """The experts of a layer on block-scaled e4m3 weights."""
     E, twoI, H = w1.shape
-    dev, I = w1.device, twoI // 2
-    _need("x", x, (torch.bfloat16,), (x.shape[0], H), dev)
+    I = twoI // 2
     _need("w1", w1, _F8, (E, 2 * I, H), dev)
     _need("w2", w2, _F8, (E, H, I), dev)
     _need("w1_scale", w1_scale, _F32, (E, 2 * I // 128, H // 128), dev)
     _need("w2_scale", w2_scale, _F32, (E, H // 128, I // 128), dev)
+
+
+def _check_batch(dt: int, x, logits, E: int, topk: int, out, topk_ids, topk_weights, workspace, dev) -> None:
+    """What a call brings beside x and the weights (workspace None: the library's own)."""
+    M = x.shape[0]
+    _need("router_logits", logits, _F32, (M, E), dev)
+    _need("out", out, (_INTER[dt],), (M, x.shape[1]), dev)
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev):
+        raise ValueError(f"the workspace is {workspace.dtype} on {workspace.device}, expected torch.uint8 on {dev}")
+    if topk_ids is not None:
+        _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
+    if topk_weights is not None:
+        _need("topk_weights", topk_weights, _F32, (M, topk), dev)
+
+
+def _layer_call(dt: int, what: str, dev, *args) -> None:
+    """The layer function `what`; a block-scaled layer on its tensors' device."""
+    if dt == MOE_FP8_BLOCK:
+        _call(getattr(lib(), what), what, dev, *args)
+    else:
+        check(getattr(lib(), what)(*args), what)
 
 
 def fused_moe_grouped(x, router_logits, w1, w2, topk: int, routing: Routing, x_scale=None, w1_scale=None,
@@ -318,19 +342,15 @@ def fused_moe_grouped(x, router_logits, w1, w2, topk: int, routing: Routing, x_s
     stream = _stream(x)
     dt = _layer_dtype(w1, w1_scale)
     if dt == MOE_FP8_BLOCK:
-        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
-    _need("router_logits", router_logits, _F32, (M, E), dev)
+        _check_block_weights(w1, w2, w1_scale, w2_scale, dev)
+        _need("x", x, (torch.bfloat16,), (M, H), dev)
     routing._check(E, dev)
     if workspace is None:
         need = fused_moe_workspace_size(dt, M, E, topk, H, I)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     if out is None:
         out = torch.empty((M, H), dtype=_INTER[dt], device=dev)
-    _need("out", out, (_INTER[dt],), (M, H), dev)
-    if topk_ids is not None:
-        _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
-    if topk_weights is not None:
-        _need("topk_weights", topk_weights, _F32, (M, topk), dev)
+    _check_batch(dt, x, router_logits, E, topk, out, topk_ids, topk_weights, workspace, dev)
     _call(lib().fused_moe_grouped, "fused_moe_grouped", dev, dt, _p(x), _p(x_scale), _p(router_logits), routing._ref,
           _p(w1), _p(w1_scale), _p(w2), _p(w2_scale), M, E, topk, H, I, _p(out), _p(topk_ids), _p(topk_weights),
           _p(workspace), workspace.numel(), stream)
@@ -344,16 +364,18 @@ def fused_moe(x, router_logits, w1, w2, topk: int, renormalize: bool = True, x_s
     E, twoI, _ = w1.shape
     I = twoI // 2
     dt = _layer_dtype(w1, w1_scale)
-    if dt == MOE_FP8_BLOCK:
-        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
     need = fused_moe_workspace_size(dt, M, E, topk, H, I)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((M, H), dtype=_INTER[dt], device=x.device)
-    check(lib().fused_moe(dt, _p(x), _p(x_scale), _p(router_logits), _p(w1), _p(w1_scale), _p(w2), _p(w2_scale),
-                          M, E, topk, H, I, int(renormalize), _p(out), _p(topk_ids), _p(topk_weights),
-                          _p(workspace), workspace.numel(), _stream(x)), "fused_moe")
+    if dt == MOE_FP8_BLOCK:
+        _check_block_weights(w1, w2, w1_scale, w2_scale, x.device)
+        _need("x", x, (torch.bfloat16,), (M, w1.shape[2]), x.device)
+        _check_batch(dt, x, router_logits, E, topk, out, topk_ids, topk_weights, workspace, x.device)
+    _layer_call(dt, "fused_moe", x.device, dt, _p(x), _p(x_scale), _p(router_logits), _p(w1), _p(w1_scale), _p(w2),
+                _p(w2_scale), M, E, topk, H, I, int(renormalize), _p(out), _p(topk_ids), _p(topk_weights),
+                _p(workspace), workspace.numel(), _stream(x))
     return out
 
 
@@ -365,13 +387,15 @@ def fused_moe_noalloc(x, router_logits, w1, w2, topk: int, renormalize: bool = T
     E, twoI, _ = w1.shape
     I = twoI // 2
     dt = _layer_dtype(w1, w1_scale)
-    if dt == MOE_FP8_BLOCK:
-        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
     if out is None:
         out = torch.empty((M, H), dtype=_INTER[dt], device=x.device)
-    check(lib().fused_moe_noalloc(dt, _p(x), _p(x_scale), _p(router_logits), _p(w1), _p(w1_scale), _p(w2),
-                                  _p(w2_scale), M, E, topk, H, I, int(renormalize), _p(out), _p(topk_ids),
-                                  _p(topk_weights), _stream(x)), "fused_moe_noalloc")
+    if dt == MOE_FP8_BLOCK:
+        _check_block_weights(w1, w2, w1_scale, w2_scale, x.device)
+        _need("x", x, (torch.bfloat16,), (M, w1.shape[2]), x.device)
+        _check_batch(dt, x, router_logits, E, topk, out, topk_ids, topk_weights, None, x.device)
+    _layer_call(dt, "fused_moe_noalloc", x.device, dt, _p(x), _p(x_scale), _p(router_logits), _p(w1), _p(w1_scale),
+                _p(w2), _p(w2_scale), M, E, topk, H, I, int(renormalize), _p(out), _p(topk_ids), _p(topk_weights),
+                _stream(x))
     return out
 
 
@@ -396,8 +420,6 @@ def fused_moe_router(x, router_w, w1, w2, topk: int, renormalize: bool = True, x
     E, twoI, _ = w1.shape
     I = twoI // 2
     dt = _layer_dtype(w1, w1_scale)
-    if dt == MOE_FP8_BLOCK:
-        _check_block_layer(x, w1, w2, w1_scale, w2_scale)
     need = fused_moe_workspace_size(dt, M, E, topk, H, I)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
@@ -405,9 +427,14 @@ def fused_moe_router(x, router_w, w1, w2, topk: int, renormalize: bool = True, x
         out = torch.empty((M, H), dtype=_INTER[dt], device=x.device)
     if logits is None:
         logits = torch.empty((M, E), dtype=torch.float32, device=x.device)
-    check(lib().fused_moe_router(dt, _p(x), _p(x_scale), _p(router_w), _p(logits), _p(w1), _p(w1_scale), _p(w2),
-                                 _p(w2_scale), M, E, topk, H, I, int(renormalize), _p(out), _p(topk_ids),
-                                 _p(topk_weights), _p(workspace), workspace.numel(), _stream(x)), "fused_moe_router")
+    if dt == MOE_FP8_BLOCK:
+        _check_block_weights(w1, w2, w1_scale, w2_scale, x.device)
+        _need("x", x, (torch.bfloat16,), (M, w1.shape[2]), x.device)
+        _check_batch(dt, x, logits, E, topk, out, topk_ids, topk_weights, workspace, x.device)
+        _need("router_w", router_w, _F32, (E, H), x.device)
+    _layer_call(dt, "fused_moe_router", x.device, dt, _p(x), _p(x_scale), _p(router_w), _p(logits), _p(w1), _p(w1_scale),
+                _p(w2), _p(w2_scale), M, E, topk, H, I, int(renormalize), _p(out), _p(topk_ids), _p(topk_weights),
+                _p(workspace), workspace.numel(), _stream(x))
     return out, logits
 
 
@@ -432,6 +459,8 @@ class ExpertCache:
         parts = (w1, w2, w1_scale, w2_scale)
         if any(t is not None and t.is_cuda for t in parts):
             raise ValueError("ExpertCache takes the experts' weights on the host")
+        if self.dtype == MOE_FP8_BLOCK:
+            _check_block_weights(*(t if t is None else t.contiguous() for t in parts), w1.device)
         self.host = [None if t is None else (t.contiguous() if t.is_pinned() else t.contiguous().pin_memory())
                      for t in parts]
         self.slots = [None if t is None else torch.empty((capacity,) + tuple(t.shape[1:]), dtype=t.dtype,
@@ -470,9 +499,12 @@ class ExpertCache:
             workspace = self._ws
         if out is None:
             out = torch.empty((M, self.H), dtype=_INTER[self.dtype], device=x.device)
-        check(lib().fused_moe_cached(self._h, _p(x), _p(x_scale), _p(router_logits), M, topk, int(renormalize),
-                                     _p(out), _p(topk_ids), _p(topk_weights), _p(self._host_ids), _p(workspace),
-                                     workspace.numel(), _stream(x)), "fused_moe_cached")
+        if self.dtype == MOE_FP8_BLOCK:
+            _need("x", x, (torch.bfloat16,), (M, self.H), self.device)
+            _check_batch(self.dtype, x, router_logits, self.E, topk, out, topk_ids, topk_weights, workspace, self.device)
+        _layer_call(self.dtype, "fused_moe_cached", self.device, self._h, _p(x), _p(x_scale), _p(router_logits), M, topk,
+                    int(renormalize), _p(out), _p(topk_ids), _p(topk_weights), _p(self._host_ids), _p(workspace),
+                    workspace.numel(), _stream(x))
         return out
 
     def close(self) -> None:

@@ -6,6 +6,7 @@
 // One block of 128 k is one f8f6f4 MFMA step (two of 64 on the 32-row form):
 // its products are summed on the matrix core from zero, and the sum joins the
 // float32 accumulator through one fused multiply-add with sa * sw.
+#include <atomic>
 #include <type_traits>
 
 #include "moe_block.h"
@@ -422,10 +423,19 @@ template <bool GATE, class C, bool NTW, bool FAR>
 static hipError_t launch_tile(const BlockArgs& a, int64_t cap, hipStream_t s) {
     const int m_tiles = (int)(cap / C::BM), n_tiles = (a.N + C::BN - 1) / C::BN;
     const int64_t nb = (int64_t)m_tiles * n_tiles;
-    static const hipError_t attr =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&block_tile_kernel<GATE, C, NTW, FAR>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, C::LdsBytes);
-    if (attr != hipSuccess) return attr;
+    if (nb > 0x7fffffffll - 8) return hipErrorInvalidValue;
+    // LDS above the default dynamic limit is requested once per kernel and device
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    hipError_t st = hipGetDevice(&dev);
+    if (st != hipSuccess) return st;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        st = hipFuncSetAttribute(reinterpret_cast<const void*>(&block_tile_kernel<GATE, C, NTW, FAR>),
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, C::LdsBytes);
+        if (st != hipSuccess) return st;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     const int group_n = (!GATE || a.one_tile) ? 1 : (n_tiles <= 8 ? n_tiles : 2);
     hipLaunchKernelGGL((block_tile_kernel<GATE, C, NTW, FAR>), dim3((unsigned)((nb + 7) / 8 * 8)), dim3(C::Threads),
                        C::LdsBytes, s, a, m_tiles, n_tiles, group_n);
