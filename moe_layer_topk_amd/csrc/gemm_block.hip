@@ -24,7 +24,7 @@ struct BlockArgs {
     const int32_t* counts;
     const int32_t* offsets;
     const int32_t* active;
-    const int32_t* num_active;
+    const int32_t* rows_end;  // the last expert's end in the sorted order
     int topk, N, K, P, block_m;
     void* c;
     float* c_scale;
@@ -78,6 +78,11 @@ struct BtCfg {
     static_assert(LdsBytes <= 160 * 1024, "LDS");
 };
 
+// silu(g) u with the hardware's reciprocal (off by 2^-23 of the value, as far as
+// the exponential): a correctly rounded quotient is nine instructions more, of
+// the seventeen a value costs.  Below g = -87 the result is 0 or -0.
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u; }
+
 // e4m3 codes of a 16-byte chunk as two bfloat16 MFMA operands (exact)
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t cvt2(uint32_t w, bool hi) {
@@ -102,17 +107,21 @@ __device__ __forceinline__ f32x4 mfma_bf16_chunk(const uint4& a, const uint4& b,
 }
 
 typedef const float __attribute__((address_space(4))) const_f32;  // uniform loads through the scalar cache
+typedef const int __attribute__((address_space(4))) const_i32;
 
 template <bool GATE, class C, bool NTW, bool FAR>
-__global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int m_tiles, int n_tiles, int group_n) {
+__global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int n_tiles, int group_n) {
     extern __shared__ __attribute__((aligned(1024))) char bt_lds[];
-    // flat tile order in groups of group_n weight tiles, cut into one
-    // contiguous range per XCD
+    // flat order of the batch's row tiles x weight tiles in groups of group_n
+    // weight tiles, cut into one contiguous range per XCD (of the tiles that
+    // exist: with the spare ones of the alignment's capacity counted, a range
+    // may hold many more than another)
     constexpr int kXcds = 8;
+    const int m_tiles = *(const_i32*)(uintptr_t)g.rows_end / C::BM;
     const int nb = m_tiles * n_tiles;
     const int per = (nb + kXcds - 1) / kXcds;
-    const int t = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-    if (t >= nb) return;
+    const int at = blockIdx.x / kXcds, t = (blockIdx.x % kXcds) * per + at;
+    if (at >= per || t >= nb) return;
     const int ng = t / (group_n * m_tiles);
     const int gw = min(group_n, n_tiles - ng * group_n);
     const int rem = t - ng * group_n * m_tiles;
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
             unsigned m = 0;
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
-                acc[0][j][v] = silu(acc[0][j][v]) * acc[1][j][v];
+                acc[0][j][v] = silu_mul(acc[0][j][v], acc[1][j][v]);
                 m = max(m, __float_as_uint(acc[0][j][v]) & 0x7fffffffu);
             }
             m = max(m, (unsigned)__shfl_xor((int)m, 32, 64));
@@ -384,10 +393,14 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
         for (int j = 0; j < C::TN; ++j) {
             const int r = trow[j];
             const BlockQuant bq(max(max(amax_s[r], amax_s[C::BM + r]), max(amax_s[2 * C::BM + r], amax_s[3 * C::BM + r])));
+            const float inv = 1.0f / fmaxf(bq.scale, kMinBlockScale);
+            auto code = [&](float x) { return __builtin_amdgcn_fmed3f(x * inv, -448.0f, 448.0f); };
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint32_t*>(bt_lds + r * kStride + 32 * wm + 8 * q + 4 * khalf) =
-                    bq.pack4(acc[0][j][4 * q], acc[0][j][4 * q + 1], acc[0][j][4 * q + 2], acc[0][j][4 * q + 3]);
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t w = pack_fp8x4(code(acc[0][j][4 * q]), code(acc[0][j][4 * q + 1]), code(acc[0][j][4 * q + 2]),
+                                              code(acc[0][j][4 * q + 3]));
+                *reinterpret_cast<uint32_t*>(bt_lds + r * kStride + 32 * wm + 8 * q + 4 * khalf) = bq.bad ? 0x7f7f7f7fu : w;
+            }
             const int p = ids_s[r];
             if (wm == 0 && khalf == 0 && p < P) g.c_scale[(size_t)p * (I / 128) + n0 / 128] = bq.scale;
         }
@@ -438,7 +451,7 @@ static hipError_t launch_tile(const BlockArgs& a, int64_t cap, hipStream_t s) {
     }
     const int group_n = (!GATE || a.one_tile) ? 1 : (n_tiles <= 8 ? n_tiles : 2);
     hipLaunchKernelGGL((block_tile_kernel<GATE, C, NTW, FAR>), dim3((unsigned)((nb + 7) / 8 * 8)), dim3(C::Threads),
-                       C::LdsBytes, s, a, m_tiles, n_tiles, group_n);
+                       C::LdsBytes, s, a, n_tiles, group_n);
     return hipGetLastError();
 }
 
@@ -786,7 +799,7 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     if (c.M == 0) return hipSuccess;
     const int P = c.M * c.topk;
     const BlockArgs a{c.a, c.a_scale, static_cast<const uint8_t*>(c.w), c.w_scale, c.al.sorted_ids, c.al.tile_expert,
-                      c.al.expert_counts, c.al.expert_offsets, c.al.active_experts, c.al.num_active, c.topk, c.N, c.K,
+                      c.al.expert_counts, c.al.expert_offsets, c.al.active_experts, c.al.expert_offsets + c.E, c.topk, c.N, c.K,
                       P, c.block_m, c.c, c.c_scale, c.ksplit, c.cpart, c.ids, P <= 64L * c.E};
     const int slots = P < c.E ? P : c.E;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
