@@ -126,11 +126,15 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
     const int gw = min(group_n, n_tiles - ng * group_n);
     const int rem = t - ng * group_n * m_tiles;
     const int mtile = rem / gw, ntile = ng * group_n + rem % gw;
-    const int e = g.tile_expert[mtile];
-    if (e < 0) return;
-
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // everything the tile's addresses need, in as few round trips as they allow
+    const int e = ((const_i32*)(uintptr_t)g.tile_expert)[__builtin_amdgcn_readfirstlane(mtile)];
+    const int lrow = lane >> 3, lphys = lane & 7;
+    int pid = g.sorted[mtile * C::BM + tid % C::BM], pa[C::ALoads];
+#pragma unroll
+    for (int j = 0; j < C::ALoads; ++j) pa[j] = g.sorted[mtile * C::BM + (wave * C::ALoads + j) * 8 + lrow];
+    const int nreal = min(C::BM, ((const_i32*)(uintptr_t)g.offsets)[e] + ((const_i32*)(uintptr_t)g.counts)[e] - mtile * C::BM);
     const int wm = wave % C::WM, wn = wave / C::WM;
     const int K = g.K, N = g.N, I = N / 2, P = g.P, nk = K / 128;
     const int n0 = ntile * (GATE ? 128 : C::BN);
@@ -138,23 +142,20 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
     int* ids_s = reinterpret_cast<int*>(bt_lds + C::IdOff);
 
     // padding rows read the tile's first row (always real); their output is dropped
-    const int p0 = g.sorted[mtile * C::BM];
-    for (int i = tid; i < 64 * C::SWaves; i += C::Threads) {
-        int p = i < C::BM ? g.sorted[mtile * C::BM + i] : P;
-        if (i < C::BM) ids_s[i] = p;
-        if (p >= P) p = p0;
-        rows_s[i] = GATE ? p / g.topk : p;
+    const int p0 = ((const_i32*)(uintptr_t)g.sorted)[__builtin_amdgcn_readfirstlane(mtile) * C::BM];
+    if (tid < 64 * C::SWaves) {
+        if (tid < C::BM) ids_s[tid] = pid;
+        if (pid >= P) pid = p0;
+        rows_s[tid] = GATE ? pid / g.topk : pid;
     }
 
     // sources of this wave's copies: instruction i fills rows 8 i .. 8 i + 7
-    const int lrow = lane >> 3, lphys = lane & 7;
     unsigned asrc[C::ALoads];
     const char* afar[C::ALoads];
 #pragma unroll
     for (int j = 0; j < C::ALoads; ++j) {
         const int r = (wave * C::ALoads + j) * 8 + lrow;
-        int p = g.sorted[mtile * C::BM + r];
-        if (p >= P) p = p0;
+        const int p = pa[j] >= P ? p0 : pa[j];
         const size_t off = (size_t)(GATE ? p / g.topk : p) * K + ring_swz(lphys, r) * 16;
         asrc[j] = (unsigned)off;
         afar[j] = static_cast<const char*>(g.a) + off;
@@ -188,16 +189,17 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
     // scales of chunk c (blocks 8 c ..): part q of 8 holds tokens 8 (q SWaves +
     // wave) ..; further waves repeat the first ones' copy (the same bytes to the
     // same place), so that a stage has no branch and every wave counts alike
-    auto issue_scales = [&](int c, int q) __attribute__((always_inline)) {
+    auto scale_copy = [&](int c, int q, int row) __attribute__((always_inline)) {
         const int i = (q * C::SWaves + wave % C::SWaves) * 8;
-        const int row = rows_s[i + (lane >> 3)];
         const int kb = min(8 * c + (lane & 7), nk - 1);
         lds_dma4_at(g.a_scale + (size_t)row * nk + kb, lds0 + C::ScaleOff + (c % 3) * C::SBuf + i * 32);
+    };
+    auto issue_scales = [&](int c, int q) __attribute__((always_inline)) {
+        scale_copy(c, q, rows_s[(q * C::SWaves + wave % C::SWaves) * 8 + (lane >> 3)]);
     };
     __syncthreads();
     // this wave's own loads above have to be done before its copies are counted
     wait_vm<0>();
-    for (int q = 0; q < 8; ++q) issue_scales(0, q);
     // copies [j0, j1) of stage kt; the last is one part of the next chunk's scales
     auto issue = [&](int kt, int j0, int j1) __attribute__((always_inline)) {
 #pragma unroll
@@ -205,8 +207,16 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
             if (j >= j0 && j < j1) issue_one(kt, j);
         if (j0 <= C::L && C::L < j1) issue_scales(kt / 8 + 1, kt % 8);
     };
+    issue(0, 0, C::L + 1);
+    {
+        int row[8];
 #pragma unroll
-    for (int s0 = 0; s0 < C::ST - 1; ++s0)
+        for (int q = 0; q < 8; ++q) row[q] = rows_s[(q * C::SWaves + wave % C::SWaves) * 8 + (lane >> 3)];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) scale_copy(0, q, row[q]);
+    }
+#pragma unroll
+    for (int s0 = 1; s0 < C::ST - 1; ++s0)
         if (s0 < nk) issue(s0, 0, C::L + 1);
 
     // wave tile: rows of the weights (row operand), tokens (column operand)
@@ -215,7 +225,6 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
     int trow[C::TN];
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) trow[j] = (wn * C::TN + j) * 32 + l31;
-    const int nreal = min(C::BM, g.offsets[e] + g.counts[e] - mtile * C::BM);
     const int live = __builtin_amdgcn_readfirstlane(min(C::TN, max(0, (nreal - wn * C::TN * 32 + 31) / 32)));
     // weight scales of this wave's rows: GATE a gate and an up block, DOWN one block
     const float* sexp = g.w_scale + (size_t)e * (N / 128) * nk;
