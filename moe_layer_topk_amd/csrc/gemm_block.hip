@@ -458,7 +458,16 @@ static hipError_t launch_tile(const BlockArgs& a, int64_t cap, hipStream_t s) {
         if (st != hipSuccess) return st;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int group_n = (!GATE || a.one_tile) ? 1 : (n_tiles <= 8 ? n_tiles : 2);
+    // Weight tiles a row tile meets before the next row tile.  Several row tiles
+    // an expert: eight, so that the 32 or 64 workgroups of an XCD share a few of
+    // both in its L2 (one / eight / all, us: gate/up of 8 experts of 4096 x 14336
+    // at 4096 tokens 1919 / 1865 / 2188, down 736 / 655 / 813; of 128 of 2048 x 768
+    // 317 / 253 / 253, 145 / 129 / 134).  One: all, an expert's weights as one
+    // stream (down of 64 experts of 4096 x 8192 at 32 tokens 338 / 345 / 304, at 200
+    // 379 / 391 / 336; gate/up of 256 of 7168 x 2048 at 1000 1286 / 1219 / 1178), but
+    // gate/up on 32-row tiles the experts' first weight tiles, then the second
+    // (64 of 4096 x 8192 at 32: 660 / 817 / 721; elsewhere within 3%).
+    const int group_n = !a.one_tile ? (n_tiles < 8 ? n_tiles : 8) : GATE && C::BM == 32 ? 1 : n_tiles;
     hipLaunchKernelGGL((block_tile_kernel<GATE, C, NTW, FAR>), dim3((unsigned)((nb + 7) / 8 * 8)), dim3(C::Threads),
                        C::LdsBytes, s, a, n_tiles, group_n);
     return hipGetLastError();
