@@ -271,12 +271,22 @@ __device__ __forceinline__ void align_core(GetId get_id, int P, int E, int block
         (&wbef[0][0])[i] = 0;
     }
     __syncthreads();
-    for (int p = tid; p < P; p += kAlignThreads) {
-        const int e = get_id(p);
-        if ((unsigned)e < (unsigned)E) {
-            atomicAdd(&wcnt[wave][e], 1);
-            if (p < chunk0) atomicAdd(&wbef[wave][e], 1);
+    // eight ids a thread in flight: one after another their latencies are most
+    // of the launch (32768 pairs just routed: 17.7 -> 13.3 us)
+    constexpr int kFlight = 8;
+    for (int p0 = tid; p0 < P; p0 += kFlight * kAlignThreads) {
+        int e[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int p = p0 + i * kAlignThreads;
+            e[i] = p < P ? get_id(p) : -1;
         }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if ((unsigned)e[i] < (unsigned)E) {
+                atomicAdd(&wcnt[wave][e[i]], 1);
+                if (p0 + i * kAlignThreads < chunk0) atomicAdd(&wbef[wave][e[i]], 1);
+            }
     }
     __syncthreads();
     for (int e = tid; e < kMaxE; e += kAlignThreads) {
