@@ -5,12 +5,14 @@
 //
 // One block of 128 k is one f8f6f4 MFMA step (two of 64 on the 32-row form):
 // its products are summed on the matrix core from zero, and the sum joins the
-// float32 accumulator through one fused multiply-add with sa * sw.
+// float32 accumulator through one fused multiply-add with sa * sw.  (gate/up
+// multiplies the codes as bfloat16 instead, see below.)
 #include <atomic>
 #include <type_traits>
 
 #include "moe_block.h"
 #include "moe_launch.h"
+#include "moe_route.h"
 
 namespace moe {
 
@@ -55,6 +57,19 @@ struct BlockArgs {
 // not: its result decides e4m3 codes and their scales, so it converts the codes
 // to bfloat16 (exact) and multiplies those at half the rate with full float32
 // sums.
+//
+// What bounds it.  gate/up of 8 experts of 4096 x 14336 at 4096 tokens: 1.83 ms,
+// 1.05 PFLOP/s.  Of the about 3400 cycles of a stage the products take 1860, and
+// a wavefront's conversions, fused multiply-adds and addresses, about 6.6 vector
+// instructions a product, do not all fit beside them (without the conversions
+// 1.66 ms of then 1.9, without the copies 1.58, without the multiply-adds 1.80).
+// Sixteen wavefronts, or four of 64 x 128, are slower (2.26 and 2.5 ms).  down of
+// 128 experts of 2048 x 768 at 4096 tokens: 130 us, 0.8 PFLOP/s; 70 of them are
+// the copies from L2 (1 GB), 25 the rows' way through LDS, 30 their stores (134
+// MB); half the products change nothing.  256 weight rows a tile (139 us), and
+// workgroups that stay and fetch the next tile's first stages during the
+// epilogue (126 us, gate/up spills) gain nothing.  Few rows: the weight stream,
+// 6.3 to 6.5 TB/s.
 
 template <int BM_, int BN_, int WN_, int ST_>
 struct BtCfg {
@@ -542,18 +557,35 @@ struct TokenBlock {
 // lane group of the MFMA reads is then one broadcast.  Eight
 // wavefronts share a workgroup's blocks (one token leaves the chip half empty,
 // and a wavefront's blocks run one after another).
+//
+// ROUTE >= 0 (ONE; 2 * groups mode + biased): the token is routed here too.  Every
+// workgroup's first wavefront chooses, while the others quantise their blocks;
+// one workgroup writes the ids and weights for the down launch.  Inside it takes
+// 3.3 us, as a launch of its own 4.4 and the way to the next one (layer of 256
+// experts of 2048 x 512 21.4 -> 18.7 us, of 8 of 4096 x 14336 no change).
+struct OneRoute {
+    RouteSpec r;
+    const float* logits;
+    int E;
+    int32_t* ids;
+    float* wts;
+};
+struct NoRoute {};
+
 template <bool ONE>
 constexpr int kRowsWaves = ONE ? 8 : 4;
 
-template <bool GATE, bool ONE>
-__global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(BlockArgs g) {
+template <bool GATE, bool ONE, int ROUTE = -1>
+__global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2)
+    block_rows_kernel(BlockArgs g, std::conditional_t<(ROUTE >= 0), OneRoute, NoRoute> route) {
     constexpr int W = kRowsWaves<ONE>;
     static_assert(GATE || !ONE, "one token's down GEMM is block_down_one_kernel");
+    static_assert(ONE || ROUTE < 0, "the router of one token");
     constexpr int kChunk = 16;  // blocks a wavefront quantises at a time
     const int slot = blockIdx.y;
-    int e, cnt, base;
+    int e = 0, cnt, base;
     if constexpr (ONE) {
-        e = g.ids[slot];
+        if constexpr (ROUTE < 0) e = g.ids[slot];
         cnt = 1;
         base = 0;
     } else {
@@ -570,6 +602,43 @@ __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(Blo
     const int N = g.N, K = g.K, I = N / 2, nkb = K / 128;
     const int kb0 = (int)((long)blockIdx.z * nkb / g.ksplit), kb1 = (int)((long)(blockIdx.z + 1) * nkb / g.ksplit);
     const int n0 = GATE ? blockIdx.x * 32 : blockIdx.x * 64;
+    // the wavefront's i-th block is kb0 + wave + W i
+    const int mine = kb1 - kb0 > wave ? (kb1 - kb0 - wave + W - 1) / W : 0;
+    // (ONE) the token's blocks i0 .. i0 + kChunk - 1 of this wavefront
+    auto quantise = [&](int i0) __attribute__((always_inline)) {
+        for (int i = i0; i < min(i0 + kChunk, mine); i += 4) {
+            const int ib = i + (lane >> 4), l = lane & 15;
+            const int b = kb0 + wave + W * min(ib, mine - 1);
+            float v[8];
+            load8<MOE_BF16>(g.a, 128 * (size_t)b + 8 * l, v);
+            const BlockQuant bq(row16_max_u32(amax8(v)));
+            const uint2 q = {bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
+            if (ib < mine) {
+                *reinterpret_cast<uint2*>(&one_q[wave][(ib - i0) * 128 + 8 * l]) = q;
+                if (l == 0) one_s[wave][ib - i0] = bq.scale;
+            }
+        }
+        // (read by this wavefront alone, after its own writes)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    if constexpr (ROUTE >= 0) {
+        __shared__ int slot_e;
+        if (wave == 0) {
+            const RouteWave<4, ROUTE / 2, ROUTE % 2> rw(route.r, route.E);
+            float l[4], wt;
+            int sel;
+            load_logits<4>(route.logits, false, 0, route.E, l);
+            route_grouped_token<4, ROUTE / 2, ROUTE % 2>(route.r, route.E, g.topk, l, rw, &sel, &wt);
+            if (lane == slot) slot_e = sel;
+            if (blockIdx.x == 0 && slot == 0 && lane < g.topk) {
+                route.ids[lane] = sel;
+                route.wts[lane] = wt;
+            }
+        }
+        quantise(0);
+        __syncthreads();
+        e = __builtin_amdgcn_readfirstlane(slot_e);
+    }
     const uint8_t* wexp = g.w + (size_t)e * N * K + 16 * lg;
     const float* sexp = g.w_scale + (size_t)e * (N / 128) * nkb;
     const uint8_t* wrow[4];
@@ -588,24 +657,6 @@ __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(Blo
         f32x4 acc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // the wavefront's i-th block is kb0 + wave + W i
-        const int mine = kb1 - kb0 > wave ? (kb1 - kb0 - wave + W - 1) / W : 0;
-        auto quantise = [&](int i0) __attribute__((always_inline)) {
-            for (int i = i0; i < min(i0 + kChunk, mine); i += 4) {
-                const int ib = i + (lane >> 4), l = lane & 15;
-                const int b = kb0 + wave + W * min(ib, mine - 1);
-                float v[8];
-                load8<MOE_BF16>(g.a, src * K + 128 * (size_t)b + 8 * l, v);
-                const BlockQuant bq(row16_max_u32(amax8(v)));
-                const uint2 q = {bq.pack4(v[0], v[1], v[2], v[3]), bq.pack4(v[4], v[5], v[6], v[7])};
-                if (ib < mine) {
-                    *reinterpret_cast<uint2*>(&one_q[wave][(ib - i0) * 128 + 8 * l]) = q;
-                    if (l == 0) one_s[wave][ib - i0] = bq.scale;
-                }
-            }
-            // (read by this wavefront alone, after its own writes)
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        };
         for (int i = 0; i < mine; ++i) {
             const int b = kb0 + wave + W * i;
             uint4 w[4][2], c0, c1;
@@ -619,7 +670,7 @@ __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2) block_rows_kernel(Blo
             }
             const float w0 = s0[b], w1 = s1[b];
             if constexpr (ONE) {
-                if (i % kChunk == 0) quantise(i);
+                if (i % kChunk == 0 && (ROUTE < 0 || i > 0)) quantise(i);
                 const uint8_t* q = &one_q[wave][(i % kChunk) * 128 + 16 * lg];
                 c0 = *reinterpret_cast<const uint4*>(q);
                 c1 = *reinterpret_cast<const uint4*>(q + 64);
@@ -779,9 +830,10 @@ static double active_experts(int M, int E, int topk) { return E * (1.0 - __built
 // Rows per tile (alignment) from the rows per expert.  A tile streams its
 // weights once, so the tile should hold an expert's rows; a taller one keeps
 // more LDS per workgroup than it fills.  gate/up + down, us, 32 / 64 / 128 rows:
-// 8 experts of 4096 x 14336 at 16 rows an expert 223 / 230 / 282, at 24 285 / 240
-// / 290, at 48 350 / 264 / 316, at 64 447 / 389 / 365; 128 experts of 2048 x 768 at
-// 16 122 / 128 / 142, at 20 143 / 132 / 147, at 48 245 / 183 / 175.
+// 8 experts of 4096 x 14336 at 18 rows an expert 231 / 231 / 269, at 24 233 / 234
+// / 269, at 40 388 / 260 / 288, at 64 548 / 418 / 336; 128 experts of 2048 x 768 at
+// 16 115 / 114 / 123, at 32 152 / 122 / 127, at 48 176 / 151 / 141, at 64 214 / 177
+// / 148.
 int block_tile_rows(int M, int E, int topk) {
     const long per_expert = (long)M * topk / E;
     return per_expert > 48 ? 128 : per_expert > 18 ? 64 : 32;
@@ -813,6 +865,13 @@ int block_down_ksplit(int M, int topk, int E, int N, int K) {
     return ks < 1 ? 1 : ks;
 }
 
+template <int ROUTE>
+static hipError_t launch_gate_one(const BlockArgs& a, const BlockGemmCall& c, hipStream_t s) {
+    const OneRoute r{*c.spec, c.logits, c.E, c.ids, c.wts};
+    hipLaunchKernelGGL((block_rows_kernel<true, true, ROUTE>), dim3(c.N / 64, c.topk, 1), dim3(64 * kRowsWaves<true>), 0, s, a, r);
+    return hipGetLastError();
+}
+
 hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     if (c.M == 0) return hipSuccess;
     const int P = c.M * c.topk;
@@ -822,12 +881,25 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     const int slots = P < c.E ? P : c.E;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
     if (c.kind == MOE_GEMM_GATE_UP_SILU) {
-        if (c.ids) hipLaunchKernelGGL((block_rows_kernel<true, true>), dim3(c.N / 64, slots, 1), dim3(64 * kRowsWaves<true>), 0, s, a);
-        else hipLaunchKernelGGL((block_rows_kernel<true, false>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a);
+        if (c.spec) {
+            switch (2 * group_mode(*c.spec, c.E, 4) + (c.spec->bias ? 1 : 0)) {
+                case 0: return launch_gate_one<0>(a, c, s);
+                case 1: return launch_gate_one<1>(a, c, s);
+                case 2: return launch_gate_one<2>(a, c, s);
+                case 3: return launch_gate_one<3>(a, c, s);
+                case 4: return launch_gate_one<4>(a, c, s);
+                default: return launch_gate_one<5>(a, c, s);
+            }
+        }
+        if (c.ids)
+            hipLaunchKernelGGL((block_rows_kernel<true, true>), dim3(c.N / 64, slots, 1), dim3(64 * kRowsWaves<true>), 0, s, a,
+                               NoRoute{});
+        else
+            hipLaunchKernelGGL((block_rows_kernel<true, false>), dim3(c.N / 64, slots, 1), dim3(256), 0, s, a, NoRoute{});
         return hipGetLastError();
     }
     if (c.kind == MOE_GEMM_DOWN) {
-        hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3(c.N / 64, slots, c.ksplit), dim3(256), 0, s, a, NoRoute{});
         return hipGetLastError();
     }
     const bool gate = c.kind == MOE_GEMM_GATE_UP_SILU_E4M3;

@@ -350,7 +350,8 @@ moe_status check_fused(moe_dtype dtype, const void* x, const float* x_scale, con
 moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, const void* w1, const float* w1_scale,
                        const void* w2, const float* w2_scale, int32_t M, int32_t E, int32_t topk, int32_t H,
                        int32_t I, void* out, const float* wts, const FusedLayout& L, hipStream_t s,
-                       const float* route_logits, int32_t renormalize, int32_t* route_ids, bool x_quantised) {
+                       const float* route_logits, int32_t renormalize, int32_t* route_ids, bool x_quantised,
+                       const RouteSpec* one_spec) {
     const bool fp8 = dtype == MOE_FP8_E4M3;
     const moe_dtype inter = dtype == MOE_F32 ? MOE_F32 : MOE_BF16;
     if (dtype == MOE_FP8_BLOCK) {
@@ -361,6 +362,9 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
             BlockGemmCall b1{MOE_GEMM_GATE_UP_SILU, route_ids ? x : L.xq, L.xs, w1, w1_scale, L.al, M, topk, E, 2 * I, H,
                              L.block_m, L.act, nullptr};
             b1.ids = route_ids;
+            b1.spec = one_spec;
+            b1.logits = route_logits;
+            b1.wts = const_cast<float*>(wts);
             if (launch_block_gemm(b1, s) != hipSuccess) return MOE_ERR_HIP;
             BlockGemmCall b2{MOE_GEMM_DOWN, L.act, nullptr, w2, w2_scale, L.al, M, topk, E, H, I, L.block_m, L.y, nullptr,
                              L.ksplit, L.ypart};
@@ -443,10 +447,10 @@ moe_status run_fused(moe_dtype dtype, const void* x, const float* x_scale, const
         if (router_w && launch_router_logits(xdt, x, x_scale, router_w, M, E, H, logits, s) != hipSuccess)
             return MOE_ERR_HIP;
         if (blk && M == 1 && !L.act_s) {
-            // one token: its ids are all the alignment the GEMMs need
-            if (launch_route_grouped(MOE_F32, logits, spec, M, E, topk, ids, wts, s) != hipSuccess) return MOE_ERR_HIP;
-            return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s, nullptr,
-                               renormalize, ids);
+            // one token: its ids are all the alignment the GEMMs need, and the
+            // gate/up launch routes it
+            return run_experts(dtype, x, x_scale, w1, w1_scale, w2, w2_scale, M, E, topk, H, I, out, wts, L, s, logits,
+                               renormalize, ids, false, &spec);
         }
         // block fp8: the routing launch quantises x beside it
         void* xq = blk ? L.xq : nullptr;

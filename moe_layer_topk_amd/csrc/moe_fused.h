@@ -69,6 +69,6 @@ moe_status run_experts(moe_dtype dtype, const void* x, const float* x_scale, con
                        const void* w2, const float* w2_scale, int32_t M, int32_t E, int32_t topk, int32_t H,
                        int32_t I, void* out, const float* wts, const FusedLayout& L, hipStream_t s,
                        const float* route_logits = nullptr, int32_t renormalize = 1, int32_t* route_ids = nullptr,
-                       bool x_quantised = false);
+                       bool x_quantised = false, const RouteSpec* one_spec = nullptr);
 
 }  // namespace moe

@@ -139,7 +139,12 @@ struct BlockGemmCall {
     float* cpart = nullptr;  // with ksplit > 1: float32 partials [ksplit][P][N] instead of c
     // float32-act kinds, one token: its topk ids, read instead of the alignment;
     // GATE_UP_SILU then takes a as the bfloat16 row and quantises it itself
-    const int32_t* ids = nullptr;
+    int32_t* ids = nullptr;
+    // GATE_UP_SILU with ids: the kernel routes the token from its logits first
+    // and writes ids and wts
+    const RouteSpec* spec = nullptr;
+    const float* logits = nullptr;
+    float* wts = nullptr;
 };
 hipError_t launch_block_gemm(const BlockGemmCall& g, hipStream_t s);
 
