@@ -218,8 +218,9 @@ moe_status moe_align(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E
  *         float32.  GATE_UP_SILU: a = e4m3 codes [M][K] with a_scale [M][K/128]
  *         (moe_quant_block), c = act float32 [P][I].  GATE_UP_SILU_E4M3: the
  *         same, but c = e4m3 codes [P][I] and c_amax receives their scales
- *         [P][I/128], quantised from the float32 act as moe_quant_block does.
- *         DOWN: a = act float32 [P][K], quantised on load the same way
+ *         [P][I/128]: moe_quant_block's scales of the float32 act, and codes of
+ *         act times the float32 reciprocal of the scale.
+ *         DOWN: a = act float32 [P][K], quantised on load as moe_quant_block does
  *         (a_scale NULL), c = y bfloat16.  DOWN_E4M3_ACT: a = codes [P][K],
  *         a_scale [P][K/128], c = y bfloat16.  The two kinds over float32 act
  *         stream the weights once per 16 rows of an expert (small batches);
