@@ -87,6 +87,9 @@ struct BtCfg {
     static constexpr int AmaxOff = IdOff + BM * 4;                                 // [WM][BM]
     static constexpr int LdsBytes = AmaxOff + WM * BM * 4;
     static constexpr int OutStride = 2 * BN + 16;                                  // DOWN: bytes of a staged output row
+    // wavefronts a SIMD has to hold (bounds the registers): two workgroups of
+    // eight wavefronts a CU where the LDS holds them
+    static constexpr int MinWaves = Waves == 8 && LdsBytes <= 80 * 1024 ? 4 : 1;
     static_assert(ALoads * 8 * Waves == BM && BLoads * 8 * Waves == BN, "copy split");
     static_assert(TM == 2 && TN >= 1, "one gate and one up tile per wave");
     static_assert(BM * OutStride <= ScaleOff, "staged output rows");
@@ -125,7 +128,7 @@ typedef const float __attribute__((address_space(4))) const_f32;  // uniform loa
 typedef const int __attribute__((address_space(4))) const_i32;
 
 template <bool GATE, class C, bool NTW, bool FAR>
-__global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int n_tiles, int group_n) {
+__global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(BlockArgs g, int n_tiles, int group_n) {
     extern __shared__ __attribute__((aligned(1024))) char bt_lds[];
     // flat order of the batch's row tiles x weight tiles in groups of group_n
     // weight tiles, cut into one contiguous range per XCD (of the tiles that
@@ -187,10 +190,17 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
         bsrc[j] = (unsigned)row * (unsigned)K + (unsigned)ring_swz(lphys, r) * 16u;
     }
     const unsigned lds0 = lds_addr_of(bt_lds);
+    // Stage kt multiplies block (kt + rot) mod nk.  Where the weights come from
+    // memory once (NTW), weight tiles start at different blocks: with rows a power
+    // of two apart, tiles at one block would all ask the same few channels (16
+    // experts of 4096 x 4096 at 64 tokens, gate/up 132 -> 86 us, down 60 -> 49; other
+    // sizes within 2%).  Where row tiles share them through L2 it costs 2%.
+    const int rot = NTW ? ntile % nk : 0;
+    auto block_of = [&](int kt) __attribute__((always_inline)) { return !NTW || kt + rot < nk ? kt + rot : kt + rot - nk; };
     // copy j of stage kt (0 .. L - 1: tokens, then weights)
     auto issue_one = [&](int kt, int j) __attribute__((always_inline)) {
         const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
-        const unsigned koff = (unsigned)kt * 128u;
+        const unsigned koff = (unsigned)block_of(kt) * 128u;
         if (j < C::ALoads) {
             const unsigned d = st + (wave * C::ALoads + j) * 1024;
             if constexpr (FAR) lds_dma16_at(afar[j] + koff, d);
@@ -201,12 +211,12 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
             else lds_dma16_buf(brsrc, bsrc[j - C::ALoads], koff, d);
         }
     };
-    // scales of chunk c (blocks 8 c ..): part q of 8 holds tokens 8 (q SWaves +
+    // scales of chunk c (stages 8 c ..): part q of 8 holds tokens 8 (q SWaves +
     // wave) ..; further waves repeat the first ones' copy (the same bytes to the
     // same place), so that a stage has no branch and every wave counts alike
     auto scale_copy = [&](int c, int q, int row) __attribute__((always_inline)) {
         const int i = (q * C::SWaves + wave % C::SWaves) * 8;
-        const int kb = min(8 * c + (lane & 7), nk - 1);
+        const int kb = min(block_of(8 * c + (lane & 7)), nk - 1);
         lds_dma4_at(g.a_scale + (size_t)row * nk + kb, lds0 + C::ScaleOff + (c % 3) * C::SBuf + i * 32);
     };
     auto issue_scales = [&](int c, int q) __attribute__((always_inline)) {
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(C::Threads) block_tile_kernel(BlockArgs g, int
             };
             read(0, 0);
             read(1, 1);
-            const float w0 = sw0[kt], w1 = sw1[kt];
+            const float w0 = sw0[block_of(kt)], w1 = sw1[block_of(kt)];
             float tok[LT];
 #pragma unroll
             for (int j = 0; j < LT; ++j) tok[j] = sc[trow[j] * 8];
@@ -483,10 +493,8 @@ static hipError_t launch_tile(const BlockArgs& a, int64_t cap, hipStream_t s) {
     // at 4096 tokens 1919 / 1865 / 2188, down 736 / 655 / 813; of 128 of 2048 x 768
     // 317 / 253 / 253, 145 / 129 / 134).  One: all, an expert's weights as one
     // stream (down of 64 experts of 4096 x 8192 at 32 tokens 338 / 345 / 304, at 200
-    // 379 / 391 / 336; gate/up of 256 of 7168 x 2048 at 1000 1286 / 1219 / 1178), but
-    // gate/up on 32-row tiles the experts' first weight tiles, then the second
-    // (64 of 4096 x 8192 at 32: 660 / 817 / 721; elsewhere within 3%).
-    const int group_n = !a.one_tile ? (n_tiles < 8 ? n_tiles : 8) : GATE && C::BM == 32 ? 1 : n_tiles;
+    // 379 / 391 / 336; gate/up of 256 of 7168 x 2048 at 1000 1286 / 1219 / 1178).
+    const int group_n = a.one_tile || n_tiles < 8 ? n_tiles : 8;
     hipLaunchKernelGGL((block_tile_kernel<GATE, C, NTW, FAR>), dim3((unsigned)((nb + 7) / 8 * 8)), dim3(C::Threads),
                        C::LdsBytes, s, a, n_tiles, group_n);
     return hipGetLastError();
