@@ -744,7 +744,8 @@ __global__ void __launch_bounds__(64 * kRowsWaves<ONE>, 2)
 // LDS, and out = sum over slots ascending of weight * y, y the sum of its splits
 // ascending.  act [topk][K] float32 is quantised by the wavefront that
 // multiplies it.  128 experts of 2048 x 768, top 8: 128 workgroups; 8 of 4096 x
-// 14336, top 2: 256, four splits each.
+// 14336, top 2: 256, four splits each.  12.6 MB of the former in 7.9 us: a
+// launch's floor and one chain of loads, products and sums.
 constexpr int kOneWaves = 8, kOneUnits = 16;  // units: topk * max(1, 8 / topk) <= 16
 
 __global__ void __launch_bounds__(64 * kOneWaves, 2) block_down_one_kernel(BlockArgs g, const float* __restrict__ wts,

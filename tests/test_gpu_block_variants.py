@@ -350,3 +350,24 @@ def test_quant_replayed_from_a_graph(dev):
             got = q.clone(), s.clone()
             wq, ws = moe.moe_quant_block(x, block_rows)
             assert torch.equal(got[0].view(torch.uint8), wq.view(torch.uint8)) and torch.equal(got[1], ws)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_layer_from_weights_quantised_on_the_device(dev, dtype):
+    """moe_quant_block's blocks of 128 rows, stacked by expert, are the layer's weights."""
+    import moe_layer_topk_amd as moe
+    M, E, k, H, I = 24, 8, 2, 256, 384
+    g = torch.Generator().manual_seed(4)
+    w1 = (torch.randn(E, 2 * I, H, generator=g) * 0.05).to(dtype)
+    w2 = (torch.randn(E, H, I, generator=g) * 0.05).to(dtype)
+    x = torch.randn(M, H, generator=g).bfloat16()
+    lg = torch.randn(M, E, generator=g)
+    b = torch.randn(E, generator=g) * 0.05
+    q1, s1 = (torch.stack(t) for t in zip(*(moe.moe_quant_block(w.to(dev), 128) for w in w1)))
+    q2, s2 = (torch.stack(t) for t in zip(*(moe.moe_quant_block(w.to(dev), 128) for w in w2)))
+    out = moe.fused_moe_grouped(x.to(dev), lg.to(dev), q1, q2, k, moe.Routing(bias=b.to(dev), **GROUPED), w1_scale=s1, w2_scale=s2)
+    r1 = [torch.stack(t) for t in zip(*(ref.quant(w, 128) for w in w1))]
+    r2 = [torch.stack(t) for t in zip(*(ref.quant(w, 128) for w in w2))]
+    assert torch.equal(q1.cpu().view(torch.uint8), r1[0].view(torch.uint8)) and torch.equal(s2.cpu(), r2[1])
+    want, _, _ = layer_ref(x, lg, k, *r1, *r2, bias=b, **GROUPED)
+    close(out, want)
