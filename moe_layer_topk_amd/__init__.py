@@ -58,7 +58,8 @@ def _p(t):
 def _stream(t: torch.Tensor):
     if not t.is_cuda:
         raise ValueError("moe_layer_topk_amd computes on the GPU only; got a CPU tensor")
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    # (the handle alone: 0.16 us a call, with torch's stream object 2.2)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.device.index))
 
 
 def moe_dtype(t: torch.Tensor) -> int:
