@@ -595,9 +595,13 @@ hipError_t launch_align(const int32_t* ids, int M, int topk, int E, int block_m,
         return hipGetLastError();
     }
     // every workgroup reads all P ids, so their number is capped: past 64 K
-    // pairs a workgroup scatters several 1024-pair sub-chunks
+    // pairs a workgroup scatters several 1024-pair sub-chunks.  With many more
+    // rows than pairs, workgroups without pairs of their own share the rows (128
+    // experts, 128-row tiles, 1040 pairs: 11.9 -> 6.4 us; 256 and 1600: 19.1 -> 6.6)
     const int units = (P + kAlignThreads - 1) / kAlignThreads;
-    const int nblk = units < kAlignMaxBlocks ? units : kAlignMaxBlocks;
+    const int rows = (int)(cap / kAlignThreads);
+    const int want = units > rows ? units : rows;
+    const int nblk = want < kAlignMaxBlocks ? want : kAlignMaxBlocks;
     const int chunk = (units + nblk - 1) / nblk * kAlignThreads;
     hipLaunchKernelGGL(align_kernel, dim3(nblk), dim3(kAlignThreads), 0, s, ids, P, E, block_m, (int)cap,
                        out.sorted_ids, out.tile_expert, out.expert_counts, out.expert_offsets, out.active_experts,
