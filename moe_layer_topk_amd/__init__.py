@@ -70,9 +70,14 @@ def moe_dtype(t: torch.Tensor) -> int:
 
 
 def _layer_dtype(w: torch.Tensor, w_scale) -> int:
-    """The layer dtype of expert weights: e4m3 with 3-D scales is block-scaled."""
+    """The layer dtype of expert weights: e4m3 with 3-D scales is block-scaled,
+    unless they are one scale for each expert kept in three dimensions ([E, 1, 1]).
+    The two meet only where one block is a whole matrix: block-scaled then, since
+    matrices that small are no multiples of 256, as per-expert scales need."""
     if w.dtype == torch.float8_e4m3fn and w_scale is not None and w_scale.dim() == 3:
-        return MOE_FP8_BLOCK
+        E, N, K = w.shape
+        if w_scale.numel() != E or w_scale.shape == (E, N // 128, K // 128):
+            return MOE_FP8_BLOCK
     return moe_dtype(w)
 
 
