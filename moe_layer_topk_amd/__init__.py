@@ -123,19 +123,31 @@ class Routing:
                  renormalize: bool = True, scale: float = 1.0):
         if score not in self._SCORES:
             raise ValueError(f"score is one of {sorted(self._SCORES)}, got {score!r}")
+        self.args = RoutingArgs(self._SCORES[score], None, n_groups, topk_groups, group_top, int(renormalize), scale)
+        self._ref = ctypes.byref(self.args)
+        self.bias = bias
+
+    @property
+    def bias(self):
+        """The balance bias.  A program may change its values in place or set
+        another tensor; calls made after that use it."""
+        return self._bias
+
+    @bias.setter
+    def bias(self, bias) -> None:
         if bias is not None:
             if not bias.is_cuda:
                 raise ValueError("moe_layer_topk_amd computes on the GPU only; got a CPU bias")
             _need("bias", bias, _F32, (bias.numel(),), bias.device)
-        self.bias = bias  # kept alive: the calls read it
-        self.args = RoutingArgs(self._SCORES[score], None if bias is None else bias.data_ptr(), n_groups, topk_groups,
-                                group_top, int(renormalize), scale)
-        self._ref = ctypes.byref(self.args)
+        self._bias = bias  # kept alive: the calls read it
 
     def _check(self, E: int, device) -> None:
-        if self.bias is not None and (self.bias.numel() != E or self.bias.device != device):
-            raise ValueError(f"the bias has {self.bias.numel()} entries on {self.bias.device}, "
-                             f"the logits {E} experts on {device}")
+        # (at each call: a tensor's storage may have moved since it was set)
+        if self._bias is None:
+            self.args.bias = None
+        else:
+            _need("bias", self._bias, _F32, (E,), device)
+            self.args.bias = self._bias.data_ptr()
 
 
 def moe_route_grouped(logits: torch.Tensor, topk: int, routing: Routing, topk_ids=None, topk_weights=None):
