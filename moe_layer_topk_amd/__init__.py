@@ -328,6 +328,28 @@ def _check_block_weights(w1, w2, w1_scale, w2_scale, dev) -> None:
     _need("w2_scale", w2_scale, _F32, (E, H // 128, I // 128), dev)
 
 
+def _check_layer(dt: int, x, w1, w2, x_scale, w1_scale, w2_scale, dev) -> None:
+    """x and the experts of a layer of any dtype (scales of a dtype that has none
+    are left for the library to refuse)."""
+    M, H = x.shape
+    E, I = w1.shape[0], w1.shape[1] // 2
+    if dt == MOE_FP8_BLOCK:
+        _check_block_weights(w1, w2, w1_scale, w2_scale, dev)
+        _need("x", x, (torch.bfloat16,), (M, w1.shape[2]), dev)
+        return
+    per_byte = 2 if dt == MOE_W4A16 else 1  # weights in an element
+    _need("w1", w1, (w1.dtype,), (E, 2 * I, H // per_byte), dev)
+    _need("w2", w2, (w1.dtype,), (E, H, I // per_byte), dev)
+    xdt = {MOE_W4A16: (torch.bfloat16,), MOE_FP8_E4M3: _CODES}.get(dt, (w1.dtype,))
+    _need("x", x, xdt, (M, H), dev)
+    if dt == MOE_W4A16:
+        _need("w1_scale", w1_scale, _F32, (E, H // 128, 2 * I), dev)
+        _need("w2_scale", w2_scale, _F32, (E, I // 128, H), dev)
+    elif dt == MOE_FP8_E4M3:  # one number for each expert (x: one), in any shape
+        for name, t, n in (("x_scale", x_scale, 1), ("w1_scale", w1_scale, E), ("w2_scale", w2_scale, E)):
+            _need(name, t, _F32, t.shape if t is not None and t.numel() == n else (n,), dev)
+
+
 def _check_batch(dt: int, x, logits, E: int, topk: int, out, topk_ids, topk_weights, workspace, dev) -> None:
     """What a call brings beside x and the weights (workspace None: the library's own)."""
     M = x.shape[0]
@@ -359,9 +381,7 @@ def fused_moe_grouped(x, router_logits, w1, w2, topk: int, routing: Routing, x_s
     dev = x.device
     stream = _stream(x)
     dt = _layer_dtype(w1, w1_scale)
-    if dt == MOE_FP8_BLOCK:
-        _check_block_weights(w1, w2, w1_scale, w2_scale, dev)
-        _need("x", x, (torch.bfloat16,), (M, H), dev)
+    _check_layer(dt, x, w1, w2, x_scale, w1_scale, w2_scale, dev)
     routing._check(E, dev)
     if workspace is None:
         need = fused_moe_workspace_size(dt, M, E, topk, H, I)
