@@ -357,6 +357,8 @@ def _check_batch(dt: int, x, logits, E: int, topk: int, out, topk_ids, topk_weig
     _need("out", out, (_INTER[dt],), (M, x.shape[1]), dev)
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev):
         raise ValueError(f"the workspace is {workspace.dtype} on {workspace.device}, expected torch.uint8 on {dev}")
+    if workspace is not None and not workspace.is_contiguous():  # (its bytes are counted from its first)
+        raise ValueError("the workspace is not contiguous")
     if topk_ids is not None:
         _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
     if topk_weights is not None:

@@ -147,3 +147,15 @@ def test_grouped_layer_refuses_scales_it_would_misread(calls, name, scale, wrong
     with pytest.raises(ValueError):
         moe.fused_moe_grouped(topk=K, routing=moe.Routing(), **a)
     assert calls == []
+
+
+@pytest.mark.parametrize("name", DTYPES)
+def test_grouped_layer_refuses_a_workspace_smaller_than_it_looks(calls, name):
+    n = moe.fused_moe_workspace_size(moe._layer_dtype(layer_args(name)["w1"], layer_args(name).get("w1_scale")), M, E, K, H, I)
+    one = torch.zeros(1, dtype=torch.uint8)
+    for ws in (one.expand(n), one.expand(2, n), torch.zeros(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            moe.fused_moe_grouped(topk=K, routing=moe.Routing(), workspace=ws, **layer_args(name))
+    assert calls == []
+    moe.fused_moe_grouped(topk=K, routing=moe.Routing(), workspace=torch.zeros(n + 9, dtype=torch.uint8)[:n], **layer_args(name))
+    assert calls == ["fused_moe_grouped"]
