@@ -406,14 +406,6 @@ __device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, i
     float den = 1.0f;
     if (r.renormalize) {
         den = wave_sum(s);
-        if (den < 1e-30f) {
-            // scores that float32 cannot hold: the quotients still can be
-            double d = 0.0;
-            if (mine) d = soft ? (m == ninf ? 0.0 : lj == m ? 1.0 : exp((double)lj - (double)m)) : 1.0 / (1.0 + exp(-(double)lj));
-            const double sum = wave_sum(d);
-            s = sum > 0.0 ? (float)(d / sum) : 0.0f;
-            den = 1.0f;
-        }
     } else if (soft) {
         den = 0.0f;
 #pragma unroll
@@ -421,8 +413,17 @@ __device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, i
             den += (V * lane + q < E) ? (l[q] == m ? 1.0f : expf(l[q] - m)) : 0.0f;
         den = wave_sum(den);
     }
+    float w = den > 0.0f ? s / den * r.scale : 0.0f;
+    if (__ballot(mine && s < 1e-30f && lj > ninf)) {
+        // a score that float32 holds badly or not at all: its weight may still be
+        // one that it holds (the sum or the factor brings it back)
+        double d = 0.0;
+        if (mine) d = soft ? (m == ninf ? 0.0 : lj == m ? 1.0 : exp((double)lj - (double)m)) : 1.0 / (1.0 + exp(-(double)lj));
+        const double sum = r.renormalize ? wave_sum(d) : (double)den;
+        w = sum > 0.0 ? (float)(d / sum * (double)r.scale) : 0.0f;
+    }
     *sel_out = sel;
-    *w_out = s / den * r.scale;
+    *w_out = w;
 }
 
 }  // namespace moe
