@@ -123,6 +123,9 @@ class Routing:
                  renormalize: bool = True, scale: float = 1.0):
         if score not in self._SCORES:
             raise ValueError(f"score is one of {sorted(self._SCORES)}, got {score!r}")
+        for name, v in (("n_groups", n_groups), ("topk_groups", topk_groups), ("group_top", group_top)):
+            if not 0 <= v < 2 ** 31:  # (ctypes would take it modulo 2^32)
+                raise ValueError(f"{name} is {v}")
         self.args = RoutingArgs(self._SCORES[score], None, n_groups, topk_groups, group_top, int(renormalize), scale)
         self._ref = ctypes.byref(self.args)
         self.bias = bias

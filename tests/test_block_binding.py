@@ -68,6 +68,13 @@ def test_routing_refuses_a_bias_it_cannot_read():
     assert (moe.Routing("sigmoid", r.bias, 4, 2, 2, False, 2.5).args.n_groups == 4)
 
 
+@pytest.mark.parametrize("name", ["n_groups", "topk_groups", "group_top"])
+@pytest.mark.parametrize("v", [2 ** 32 + 1, 2 ** 31, -2 ** 32 + 1, -1])
+def test_routing_refuses_numbers_it_would_cut(name, v):
+    with pytest.raises(ValueError, match=name):
+        moe.Routing(**{name: v})
+
+
 # ------------------------------------------------- fused_moe_grouped, any dtype
 
 E, K, H, I, M = 4, 2, 512, 256, 3
