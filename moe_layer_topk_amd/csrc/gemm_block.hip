@@ -27,7 +27,7 @@ struct BlockArgs {
     const int32_t* offsets;
     const int32_t* active;
     const int32_t* rows_end;  // the last expert's end in the sorted order
-    int topk, N, K, P, block_m;
+    int topk, N, K, P;
     void* c;
     float* c_scale;
     int ksplit;
@@ -38,9 +38,9 @@ struct BlockArgs {
 
 // ------------------------------------------------------------ e4m3 act (tiles)
 //
-// Block tile: 256 weight rows (GATE: 128 gate rows and the matching 128 up
-// rows, so one workgroup holds whole 128-column blocks of act and can quantise
-// them) x BM sorted token rows x 128 k.  Weights on the MFMA row operand,
+// Block tile: BM sorted token rows x 128 k x BN weight rows (DOWN: 128; GATE:
+// 256, 128 gate rows and the matching 128 up rows, so one workgroup holds whole
+// 128-column blocks of act and can quantise them).  Weights on the MFMA row operand,
 // tokens on the column operand: a lane's accumulators all belong to one token,
 // so a block's scale sa * sw is one number per 32 x 32 tile.
 //
@@ -129,6 +129,7 @@ typedef const int __attribute__((address_space(4))) const_i32;
 
 template <bool GATE, class C, bool NTW, bool FAR>
 __global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(BlockArgs g, int n_tiles, int group_n) {
+    static_assert(C::BN == (GATE ? 256 : 128), "whole tiles of N, one block of weight scales for each 128 rows");
     extern __shared__ __attribute__((aligned(1024))) char bt_lds[];
     // flat order of the batch's row tiles x weight tiles in groups of group_n
     // weight tiles, cut into one contiguous range per XCD (of the tiles that
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(Blo
     const int nreal = min(C::BM, ((const_i32*)(uintptr_t)g.offsets)[e] + ((const_i32*)(uintptr_t)g.counts)[e] - mtile * C::BM);
     const int wm = wave % C::WM, wn = wave / C::WM;
     const int K = g.K, N = g.N, I = N / 2, P = g.P, nk = K / 128;
-    const int n0 = ntile * (GATE ? 128 : C::BN);
+    const int n0 = ntile * 128;
     int* rows_s = reinterpret_cast<int*>(bt_lds + C::RowOff);
     int* ids_s = reinterpret_cast<int*>(bt_lds + C::IdOff);
 
@@ -185,8 +186,7 @@ __global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(Blo
 #pragma unroll
     for (int j = 0; j < C::BLoads; ++j) {
         const int r = (wave * C::BLoads + j) * 8 + lrow;
-        int row = GATE ? (r < 128 ? n0 + r : I + n0 + r - 128) : n0 + r;
-        if (!GATE && row >= N) row = N - 1;  // N an odd multiple of 128: the last tile's upper half is dropped
+        const int row = GATE && r >= 128 ? I + n0 + r - 128 : n0 + r;
         bsrc[j] = (unsigned)row * (unsigned)K + (unsigned)ring_swz(lphys, r) * 16u;
     }
     const unsigned lds0 = lds_addr_of(bt_lds);
@@ -251,10 +251,9 @@ __global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(Blo
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) trow[j] = (wn * C::TN + j) * 32 + l31;
     const int live = __builtin_amdgcn_readfirstlane(min(C::TN, max(0, (nreal - wn * C::TN * 32 + 31) / 32)));
-    // weight scales of this wave's rows: GATE a gate and an up block, DOWN one block
+    // weight scales of the tile: GATE a gate and an up block, DOWN one block
     const float* sexp = g.w_scale + (size_t)e * (N / 128) * nk;
-    const int nblk = GATE ? n0 / 128 : min((n0 + 64 * wm) / 128, N / 128 - 1);
-    const_f32* sw0 = (const_f32*)(uintptr_t)(sexp + (size_t)__builtin_amdgcn_readfirstlane(nblk) * nk);
+    const_f32* sw0 = (const_f32*)(uintptr_t)(sexp + (size_t)__builtin_amdgcn_readfirstlane(n0 / 128) * nk);
     const_f32* sw1 = GATE ? sw0 + (size_t)(I / 128) * nk : sw0;
 
     f32x16 acc[C::TM][C::TN];
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(Blo
         constexpr int kVecs = C::BN / 8;  // 16-byte pieces of a row
         for (int i = tid; i < C::BM * kVecs; i += C::Threads) {
             const int r = i / kVecs, v = i % kVecs, n = n0 + 8 * v, p = ids_s[r];
-            if (p < P && n < N)
+            if (p < P)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.c) + (size_t)p * N + n) =
                     *reinterpret_cast<const uint4*>(bt_lds + r * C::OutStride + 16 * v);
         }
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(C::Threads, C::MinWaves) block_tile_kernel(Blo
 
 template <bool GATE, class C, bool NTW, bool FAR>
 static hipError_t launch_tile(const BlockArgs& a, int64_t cap, hipStream_t s) {
-    const int m_tiles = (int)(cap / C::BM), n_tiles = (a.N + C::BN - 1) / C::BN;
+    const int m_tiles = (int)(cap / C::BM), n_tiles = a.N / C::BN;
     const int64_t nb = (int64_t)m_tiles * n_tiles;
     if (nb > 0x7fffffffll - 8) return hipErrorInvalidValue;
     // LDS above the default dynamic limit is requested once per kernel and device
@@ -861,8 +860,7 @@ bool block_tile_rows_ok(int block_m) { return block_m == 32 || block_m == 64 || 
 // rows / tiles: 128 experts of 2048 x 768 at 16 tokens (492 workgroups) 69 / 85,
 // at 64 (756) 114 / 113; 8 of 4096 x 1024 at 8 rows an expert 26 / 41, at 16
 // 40 / 42; 64 of 4096 x 8192 at one token (512) 154 / 134, at 4 465 / 408.
-bool block_f32_act(int M, int E, int topk, int H, int I) {
-    (void)H;
+bool block_f32_act(int M, int E, int topk, int I) {
     return (long)M * topk <= 8L * E && (I / 128) * active_experts(M, E, topk) < 512.0;
 }
 
@@ -890,7 +888,7 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     const int P = c.M * c.topk;
     const BlockArgs a{c.a, c.a_scale, static_cast<const uint8_t*>(c.w), c.w_scale, c.al.sorted_ids, c.al.tile_expert,
                       c.al.expert_counts, c.al.expert_offsets, c.al.active_experts, c.al.expert_offsets + c.E, c.topk, c.N, c.K,
-                      P, c.block_m, c.c, c.c_scale, c.ksplit, c.cpart, c.ids, P <= 64L * c.E};
+                      P, c.c, c.c_scale, c.ksplit, c.cpart, c.ids, P <= 64L * c.E};
     const int slots = P < c.E ? P : c.E;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
     if (c.kind == MOE_GEMM_GATE_UP_SILU) {
@@ -923,7 +921,7 @@ hipError_t launch_block_gemm(const BlockGemmCall& c, hipStream_t s) {
     // 4096 x 14336, 256 workgroups, 73 / 108; of 128 of 2048 x 768, 1300, 36 / 29;
     // gate/up of 8 of 4096 x 1024, 64 workgroups, 30 / 44; of 128 of 2048 x 768, 756,
     // 83 / 72.  (128-row tiles: the LDS holds one shape.)
-    const double wgs = active_experts(c.M, c.E, c.topk) * (gate ? c.N / 256 : (c.N + 127) / 128);
+    const double wgs = active_experts(c.M, c.E, c.topk) * (c.N / (gate ? 256 : 128));
     if (gate) {
         if (c.block_m == 128) return launch_tile_c<true, BtCfg<128, 256, 2, 3>>(a, cap, far, s);
         if (c.block_m == 64) return launch_tile_c<true, BtCfg<64, 256, 2, 3>>(a, cap, far, s);

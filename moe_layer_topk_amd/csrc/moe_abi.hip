@@ -118,7 +118,7 @@ FusedLayout fused_layout(char* ws, moe_dtype dtype, int32_t M, int32_t E, int32_
     L.al.num_active = c.take<int32_t>(1);
     L.amax = c.take<float>(1);
     const bool blk = dtype == MOE_FP8_BLOCK;
-    const bool codes = blk && !block_f32_act(M, E, topk, H, I);  // the GEMMs pass act as codes and scales
+    const bool codes = blk && !block_f32_act(M, E, topk, I);  // the GEMMs pass act as codes and scales
     L.xq = blk ? c.take<char>((size_t)M * H) : nullptr;
     L.xs = blk ? c.take<float>((size_t)M * (H / 128)) : nullptr;
     L.act_s = codes ? c.take<float>((size_t)P * (I / 128)) : nullptr;

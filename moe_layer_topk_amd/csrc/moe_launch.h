@@ -156,7 +156,7 @@ hipError_t launch_block_down_one(const BlockGemmCall& c, const float* wts, void*
 // in float32 (ring kernels), and then the K split of the down GEMM.
 int block_tile_rows(int M, int E, int topk);
 bool block_tile_rows_ok(int block_m);
-bool block_f32_act(int M, int E, int topk, int H, int I);
+bool block_f32_act(int M, int E, int topk, int I);
 int block_down_ksplit(int M, int topk, int E, int N, int K);
 
 hipError_t launch_combine_partials(const float* ypart, int ksplit, const float* w, int M, int topk, int H,
