@@ -30,19 +30,19 @@ __device__ __forceinline__ f32x4 mfma_f8_16x16x128(const uint4& a0, const uint4&
 // per thread) and two remainder corrections by fused multiply-add: with r
 // correctly rounded, the first correction leaves the quotient within one
 // ulp and the second returns the correctly rounded quotient (Markstein's
-// theorem), provided nothing under- or overflows.  A scale below the normal
-// range is brought into it by multiplying s and every a by 2^64 (exact, and
-// the quotient is unchanged; s <= FLT_MAX/448 keeps r normal at the top);
-// quotients small enough to lose exactness in the corrections (below
-// 2^-100) quantise to zero either way.  The corrections turn a -0 quotient
+// theorem), provided nothing under- or overflows.  A remainder may be as small as
+// 2^-34 s (half a step of the smallest quotient a code hangs on), so a scale below
+// 2^-80 is raised by multiplying s and every a by 2^64 (exact, and the quotient is
+// unchanged; the smallest s, 2^-149, becomes 2^-85; s <= FLT_MAX/448 keeps r normal
+// at the top).  The corrections turn a -0 quotient
 // into +0, so the sign is taken from a (s > 0): a zero quotient keeps the
 // sign an IEEE division gives it.  Everything here is uniform across the
 // wavefront except a, so the per-value path has no branch.
 struct ActQuant {
     float pre, s, r;
     __device__ __forceinline__ explicit ActQuant(float scale) {
-        const bool sub = scale < 1.17549435e-38f;
-        pre = sub ? 18446744073709551616.0f : 1.0f;  // 2^64
+        const bool low = scale < 8.27180613e-25f;    // 2^-80
+        pre = low ? 18446744073709551616.0f : 1.0f;  // 2^64
         s = scale * pre;
         r = 1.0f / s;
     }
