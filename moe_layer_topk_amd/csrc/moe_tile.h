@@ -24,28 +24,22 @@ __device__ __forceinline__ f32x4 mfma_f8_16x16x128(const uint4& a0, const uint4&
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
-// Per-tensor e4m3 quantiser of the float32 intermediate: code = e4m3 of the
-// IEEE float32 quotient a / s (round to nearest even, saturated at +-448),
-// s = amax / 448.  The quotient is formed from r = 1/s (one IEEE division
+// e4m3 codes of the IEEE float32 quotients a / scale (round to nearest even,
+// saturated at +-448).  A quotient is formed from r = 1/s (one IEEE division
 // per thread) and two remainder corrections by fused multiply-add: with r
 // correctly rounded, the first correction leaves the quotient within one
 // ulp and the second returns the correctly rounded quotient (Markstein's
 // theorem), provided nothing under- or overflows.  A remainder may be as small as
 // 2^-34 s (half a step of the smallest quotient a code hangs on), so a scale below
 // 2^-80 is raised by multiplying s and every a by 2^64 (exact, and the quotient is
-// unchanged; the smallest s, 2^-149, becomes 2^-85; s <= FLT_MAX/448 keeps r normal
-// at the top).  The corrections turn a -0 quotient
-// into +0, so the sign is taken from a (s > 0): a zero quotient keeps the
-// sign an IEEE division gives it.  Everything here is uniform across the
-// wavefront except a, so the per-value path has no branch.
-struct ActQuant {
+// unchanged; the smallest s, 2^-149, becomes 2^-85; scale <= FLT_MAX/448 keeps r
+// normal at the top).  The corrections turn a -0 quotient into +0, so the sign is
+// taken from a (s > 0): a zero quotient keeps the sign an IEEE division gives it.  The
+// per-value path has no branch.
+struct E4m3Quant {
     float pre, s, r;
-    __device__ __forceinline__ explicit ActQuant(float scale) {
-        const bool low = scale < 8.27180613e-25f;    // 2^-80
-        pre = low ? 18446744073709551616.0f : 1.0f;  // 2^64
-        s = scale * pre;
-        r = 1.0f / s;
-    }
+    __device__ __forceinline__ explicit E4m3Quant(float scale)
+        : pre(scale < 8.27180613e-25f ? 18446744073709551616.0f : 1.0f), s(scale * pre), r(1.0f / s) {}  // 2^-80, 2^64
     __device__ __forceinline__ float quot(float a0) const {
         const float a = a0 * pre;
         float q = a * r;
@@ -55,14 +49,22 @@ struct ActQuant {
         return __builtin_copysignf(__builtin_fmaf(e, r, q), a);
     }
     __device__ __forceinline__ float sat(float a) const { return __builtin_amdgcn_fmed3f(quot(a), -448.0f, 448.0f); }
+    __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) const {
+        return pack_fp8x4(sat(a), sat(b), sat(c), sat(d));
+    }
+};
+
+// Per-tensor quantiser of the float32 intermediate, scale = amax / 448: uniform
+// across the wavefront.
+struct ActQuant : E4m3Quant {
+    using E4m3Quant::E4m3Quant;
     // 16 float32 values (four 16-byte chunks) -> 16 e4m3 codes
     __device__ __forceinline__ uint4 codes16(const uint4& v0, const uint4& v1, const uint4& v2,
                                              const uint4& v3) const {
         return uint4{pack4(v0), pack4(v1), pack4(v2), pack4(v3)};
     }
     __device__ __forceinline__ uint32_t pack4(const uint4& v) const {
-        return pack_fp8x4(sat(__uint_as_float(v.x)), sat(__uint_as_float(v.y)), sat(__uint_as_float(v.z)),
-                          sat(__uint_as_float(v.w)));
+        return E4m3Quant::pack4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
     }
 };
 
