@@ -149,9 +149,11 @@ moe_status moe_route(const float* logits, int32_t M, int32_t E, int32_t topk, in
  *     bias experts are ranked by their logits, which both scores rise with
  *     (so logits whose scores round alike keep their order);
  *  4. w_j = s_j (without the bias), / sum of the chosen s if renormalize,
- *     times scale, float32.
+ *     times scale, float32 (scores below float32's range included: only w_j
+ *     itself underflows).
  * Ids are those of exact arithmetic to float64: float32 decides where its
- * error cannot change the choice, float64 decides the rest.
+ * error cannot change the choice, float64 decides the rest (a batch of such
+ * tokens, as with an expert disabled by its bias, takes about twice as long).
  * A logit of -inf has score 0; NaN logits count as -inf, and a choice or
  * group score that is NaN ranks with -inf.  +inf logits share a softmax's
  * mass evenly.  Softmax of a row with nothing above -inf: scores 0.  Weights

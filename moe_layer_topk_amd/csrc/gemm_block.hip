@@ -58,8 +58,8 @@ struct BlockArgs {
 // to bfloat16 (exact) and multiplies those at half the rate with full float32
 // sums.
 //
-// What bounds it.  gate/up of 8 experts of 4096 x 14336 at 4096 tokens: 1.83 ms,
-// 1.05 PFLOP/s.  Of the about 3400 cycles of a stage the products take 1860, and
+// What bounds it.  gate/up of 8 experts of 4096 x 14336 at 4096 tokens: 1.86 ms,
+// 1.03 PFLOP/s.  Of the about 3400 cycles of a stage the products take 1860, and
 // a wavefront's conversions, fused multiply-adds and addresses, about 6.6 vector
 // instructions a product, do not all fit beside them (without the conversions
 // 1.66 ms of then 1.9, without the copies 1.58, without the multiply-adds 1.80).

@@ -124,7 +124,7 @@ hipError_t launch_quant_block(moe_dtype xdt, const void* x, int rows, int K, int
                               hipStream_t s);
 
 // A grouped GEMM on block-scaled e4m3 (MOE_FP8_BLOCK); the kinds pick the
-// kernels: float32 act -> the ring kernel, e4m3 act -> the tile kernel.
+// kernels: float32 act -> the rows kernels, e4m3 act -> the tile kernel.
 struct BlockGemmCall {
     moe_gemm_kind kind;
     const void* a;
@@ -136,7 +136,7 @@ struct BlockGemmCall {
     void* c;
     float* c_scale;          // GATE_UP_SILU_E4M3: scales of the codes c
     int ksplit = 1;          // DOWN over float32 act: split of K across workgroups
-    float* cpart = nullptr;  // with ksplit > 1: float32 partials [ksplit][P][N] instead of c
+    float* cpart = nullptr;  // ... float32 partials [ksplit][P][N] instead of c (needed with ksplit > 1)
     // float32-act kinds, one token: its topk ids, read instead of the alignment;
     // GATE_UP_SILU then takes a as the bfloat16 row and quantises it itself
     int32_t* ids = nullptr;
@@ -153,7 +153,7 @@ hipError_t launch_block_gemm(const BlockGemmCall& g, hipStream_t s);
 hipError_t launch_block_down_one(const BlockGemmCall& c, const float* wts, void* out, hipStream_t s);
 
 // MOE_FP8_BLOCK layers: tile height, whether the GEMMs pass the intermediate
-// in float32 (ring kernels), and then the K split of the down GEMM.
+// in float32 (rows kernels), and then the K split of the down GEMM.
 int block_tile_rows(int M, int E, int topk);
 bool block_tile_rows_ok(int block_m);
 bool block_f32_act(int M, int E, int topk, int I);

@@ -11,8 +11,16 @@
 // own error: with eta the bound of one choice, two that differ by more than
 // 4 eta are ordered as in float64.  A token with a closer pair at a place that
 // matters (neighbours among the taken, the best one left, two groups) is done
-// again in float64; on normal logits about one token in a thousand.  Without
-// a bias experts are ranked by their logits, exactly, ties included.
+// again in float64.  Without a bias experts are ranked by their logits, exactly,
+// ties included.
+//   One eta serves all comparisons of a token: it is as wide as the largest |bias|
+// makes it, and as coarse as 2^-22 beside scores that saturate.  Tokens repeated
+// in float64, 256 experts in 8 groups: 0.1% on standard normal logits with biases
+// of 0.05, 0.2% (softmax with biases of 0.002: 2%) at a deviation of 6 or 10; at 6
+// with biases of 0 97% of the sigmoids' and 20% of the softmaxes', without a bias
+// 54% and 14%; with one expert disabled by a bias of -1e4 87 to 100%, of -1e9 or
+// -inf all.  A repeated batch takes twice as long (16384 tokens: sigmoid 22 us and
+// 46, softmax 27 and 50).
 //   sigmoid: 1 / (1 + e), e = exp2(-l log2 e): the argument's rounding costs
 //     |l| 2^-24, the exponential 2^-23, and s (1 - s) |l| <= 0.23; with the sum
 //     and the reciprocal below 4 x 2^-24, plus the sum's with the bias.
@@ -393,7 +401,8 @@ __device__ __forceinline__ void route_grouped_token(const RouteSpec& r, int E, i
     if (__builtin_expect(!route_choose<float, V, GM, BIASED>(r, E, topk, l, rw, m, sel), 0))
         route_choose<double, V, GM, BIASED>(r, E, topk, l, rw, m, sel);
 
-    // the chosen experts' scores, from their logits
+    // the chosen experts' scores, from their logits: float32 exponentials, sums and
+    // quotients (6e-8 of a weight; from float64 it would be its rounding, 3e-8)
     float lj = 0.0f;
 #pragma unroll
     for (int q = 0; q < V; ++q) {

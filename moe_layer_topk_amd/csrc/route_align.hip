@@ -215,9 +215,10 @@ __device__ __forceinline__ void router_phase(const void* __restrict__ x, const f
 
 // ------------------------------------------------------------------ align
 //
-// min(ceil(P / 1024), 64) workgroups of 1024 threads, no inter-workgroup
-// traffic.  Counting sort with a stable scatter; workgroup b scatters the
-// pairs [b C, b C + C) (C = 1024 up to 64 K pairs):
+// min(max(ceil(P / 1024), cap / 1024), 64) workgroups of 1024 threads, no
+// inter-workgroup traffic.  Counting sort with a stable scatter; workgroup b
+// scatters the pairs [b C, b C + C) (C = 1024 up to 64 K pairs); workgroups past
+// the last pair share the rows alone (step 3):
 //  1. Every workgroup histograms all P expert ids, and separately the ids
 //     before its own chunk, in per-wavefront LDS counters (summed after),
 //     so it knows each expert's count and how many of the expert's pairs

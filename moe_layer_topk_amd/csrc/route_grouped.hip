@@ -8,8 +8,9 @@ namespace moe {
 // One wavefront per token, tokens in strides over at most 2048 workgroups of
 // four (32 wavefronts a CU); the next token's logits load during this one.
 // Bound by vector ALU work, about 600 instructions a token: 16384 tokens of 256
-// experts in 8 groups 22.5 us (17 MB), and no faster with more or fewer
-// wavefronts a CU; two tokens a wavefront cost as much in sorting as they save.
+// experts in 8 groups 22.6 us (17 MB; 46 where float32 settles no choice, see
+// moe_route.h), and no faster with more or fewer wavefronts a CU; two tokens a
+// wavefront cost as much in sorting as they save.
 // Workgroups past `routers` quantise the token rows (qj) the layer needs next.
 template <int V, int GM, bool BIASED>
 __global__ void __launch_bounds__(256) route_grouped_kernel(const void* __restrict__ logits, int bf16, RouteSpec r,
