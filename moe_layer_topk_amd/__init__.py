@@ -10,7 +10,8 @@ moe_route -> moe_align -> moe_grouped_gemm (gate/up + SiLU-and-mul, then
 down) -> moe_combine, or all of them in one call with fused_moe.  For e4m3
 weights the intermediate is float32 and the down call quantises it on load;
 moe_quant_act gives the same codes as a tensor.  Block-scaled e4m3 (weights
-float8_e4m3fn with 3-D float32 scales, one per 128 x 128 block): moe_quant_block
+float8_e4m3fn with float32 scales [E, N/128, K/128], one per 128 x 128 block;
+[E] or [E, 1, 1] are one scale an expert): moe_quant_block
 -> moe_grouped_gemm with the E4M3 kinds, or the fused layers from bfloat16
 hidden states.  moe_route_grouped / fused_moe_grouped route with a Routing
 (softmax or sigmoid scores, balance bias, expert groups).
@@ -133,7 +134,8 @@ class Routing:
     @property
     def bias(self):
         """The balance bias.  A program may change its values in place or set
-        another tensor; calls made after that use it."""
+        another tensor; calls made after that use it.  A captured call goes on
+        reading the tensor it was captured with, which has to live as long."""
         return self._bias
 
     @bias.setter
