@@ -64,8 +64,9 @@ typedef enum {
     MOE_GEMM_GATE_UP_SILU = 0, /* act[p] = silu(W1[e][0:I] x) * (W1[e][I:2I] x) */
     MOE_GEMM_DOWN = 1,         /* y[p]   = W2[e] act[p]                         */
     MOE_GEMM_DOWN_E4M3_ACT = 2, /* as DOWN, act given as e4m3 codes (moe_quant_act) */
-    MOE_GEMM_GATE_UP_SILU_E4M3 = 3 /* MOE_FP8_BLOCK only: as GATE_UP_SILU, act as e4m3
-                                      codes with a scale per 128 columns of a row */
+    MOE_GEMM_GATE_UP_SILU_E4M3 = 3, /* MOE_FP8_BLOCK only: as GATE_UP_SILU, act as e4m3
+                                       codes with a scale per 128 columns of a row */
+    MOE_GEMM_GATE_UP = 4 /* MOE_BF16 only: z[p] = W1[e] x, gate and up before SiLU-and-mul */
 } moe_gemm_kind;
 
 /* Scores a router's logits turn into (moe_routing). */
@@ -190,6 +191,11 @@ moe_status moe_align(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E
  *         0..I-1, up rows I..2I-1), c = act [P][I] in pair order.
  *  kind = MOE_GEMM_DOWN: a = act [P][K=I], w = W2 [E][N=H][K], c = y [P][N] in
  *         pair order.
+ *  kind = MOE_GEMM_GATE_UP (MOE_BF16): a = x [M][K=H], w = W1 [E][N=2I][K],
+ *         c = z [P][N] bfloat16, gate columns 0..I-1 and up columns I..2I-1:
+ *         what a backward pass through SiLU-and-mul needs (moe_grouped_gemm_dx).
+ *         block_m 64 or 128; x or one expert's weights of 4 GiB or more ->
+ *         MOE_ERR_UNSUPPORTED.
  *  dtype: MOE_F32 (a, w, c float32), MOE_BF16 (a, w, c bfloat16),
  *         MOE_FP8_E4M3 (w e4m3 with w_scale[E] float32 per expert matrix;
  *         GATE_UP: a = x e4m3 with a_scale -> its float32 scale, c = act
@@ -375,6 +381,134 @@ moe_status fused_moe_noalloc(moe_dtype dtype, const void* x, const float* x_scal
 
 /* MOE_NOALLOC_SCRATCH_BYTES, as a call (for bindings that cannot read macros). */
 size_t fused_moe_noalloc_scratch_bytes(void);
+
+/* ------------------------------------------------------ around the experts
+ * What a block has beside its experts' products, and what a training step
+ * takes back through all of it.  Rows in expert order: row r of the sorted
+ * list holds the pair sorted_ids[r] (moe_align), so an expert's rows are
+ * contiguous, for programs that send them elsewhere or multiply them
+ * themselves.  moe_grouped_gemm needs no such rows: it reads tokens and writes
+ * pair order (row p of pair p), which the calls below take as pair_row NULL.
+ *
+ * moe_permute: token rows to expert order, with a weight each if given.
+ *   rows[r] = w_p * x[p / topk] for every r that holds a pair p; the padding rows
+ *   of the experts' runs are zeros; rows past the padded total are left as they
+ *   were.  pair_row[p] = r, or -1 for a pair whose id is no expert.
+ *  dtype     MOE_F32 or MOE_BF16, of x and rows
+ *  x         device [M][H]
+ *  weights   device float32 [M][topk], or NULL (rows are copies)
+ *  topk_ids, al, block_m   the ids and what moe_align made of them
+ *  rows      device [moe_align_capacity(M, topk, E, block_m)][H]
+ *  pair_row  device int32 [M][topk]
+ * H must be a multiple of 8 (MOE_ERR_SHAPE).  Errors as for moe_align; at most
+ * 2^23 tokens and 2^28 rows (MOE_ERR_UNSUPPORTED). */
+moe_status moe_permute(moe_dtype dtype, const void* x, const float* weights, const int32_t* topk_ids,
+                       const moe_align_bufs* al, int32_t M, int32_t topk, int32_t E, int32_t block_m, int32_t H,
+                       void* rows, int32_t* pair_row, void* stream);
+
+/* Expert rows back to token order:
+ *   out[t] = sum_j w_tj * rows[pair_row[t][j]], j ascending, float32 sums,
+ * weights NULL: 1; a pair_row outside [0, nrows) adds nothing (a pair with no
+ * expert).  pair_row NULL: pair order, nrows = M topk.
+ *  rows  device [nrows][H] in dtype; out device [M][H] in out_dtype (each
+ *        MOE_F32 or MOE_BF16). */
+moe_status moe_unpermute(moe_dtype dtype, const void* rows, int64_t nrows, const int32_t* pair_row,
+                         const float* weights, int32_t M, int32_t topk, int32_t H, moe_dtype out_dtype, void* out,
+                         void* stream);
+
+/* Gradients of moe_unpermute (and, with pair_row NULL, of moe_combine) from
+ * dout, the gradient of out:
+ *   drows[r] = w_p * dout[p / topk],  dweights[p] = <rows[r], dout[p / topk]>, r = pair_row[p]
+ * (float32 sums; dweights 0 for a pair with no row).  drows may be rows.
+ *  dout      device [M][H], rows and drows [nrows][H], all in dtype
+ *  weights   NULL: 1 (then dweights must be NULL)
+ *  rows, dweights   NULL together: no gradient of the weights
+ *  al        non-NULL (needs pair_row): the padding rows of the experts' runs
+ *            become zeros, as products over whole tiles of drows need; E and
+ *            block_m are read only then, and nrows is the capacity.  Rows that
+ *            are neither a pair's nor zeroed are left as they were. */
+moe_status moe_unpermute_backward(moe_dtype dtype, const void* dout, const void* rows, int64_t nrows,
+                                  const int32_t* pair_row, const float* weights, const moe_align_bufs* al, int32_t M,
+                                  int32_t topk, int32_t E, int32_t block_m, int32_t H, void* drows, float* dweights,
+                                  void* stream);
+
+/* Gradients of moe_permute from drows, the gradient of rows:
+ *   dx[t] = sum_j w_tj * drows[pair_row[t][j]],  dweights[p] = <drows[pair_row[p]], x[p / topk]>
+ * j ascending, float32 sums; pairs with no row give 0.  With pair_row NULL and no
+ * weights it sums the pair rows of moe_grouped_gemm_dx over the topk experts.
+ *  x, dweights  NULL together (no gradient of the weights); else weights non-NULL
+ *  drows device [nrows][H], x and dx device [M][H], in dtype. */
+moe_status moe_permute_backward(moe_dtype dtype, const void* drows, int64_t nrows, const int32_t* pair_row,
+                                const void* x, const float* weights, int32_t M, int32_t topk, int32_t H, void* dx,
+                                float* dweights, void* stream);
+
+/* The norms around a block with its gate and residual scale (moe_residual_norm). */
+typedef struct {
+    const void* post_weight; /* [H] norm after the block, or NULL: none            */
+    const void* gate;        /* [H], or [M] with gate_per_token, or NULL: 1         */
+    const void* pre_weight;  /* [H] norm before the next block, or NULL: none       */
+    moe_dtype w_dtype;       /* of the three: MOE_F32 or MOE_BF16                  */
+    int32_t gate_per_token;
+    float scale;             /* residual scale, finite */
+    float eps;               /* added to the mean squares, finite, > 0 */
+} moe_norm_spec;
+
+/* One pass over the rows between two blocks:
+ *   u     = y * (mean(y^2) + eps)^-1/2 * post_weight      (post_weight NULL: u = y)
+ *   h_out = h + scale * gate * u
+ *   x     = h_out * (mean(h_out^2) + eps)^-1/2 * pre_weight
+ * in float32 from the inputs to each output (x does not see h_out's rounding).
+ *  dtype  MOE_F32 or MOE_BF16, of h, y, h_out and x, all device [M][H]
+ *  y      the block's output; NULL: h_out = h, and h_out, post_weight and gate
+ *         must be NULL (only x is written)
+ *  x      NULL exactly when pre_weight is
+ * An output may be one of the inputs h and y; the outputs differ.  H must be a multiple of 8
+ * (MOE_ERR_SHAPE) of at most 16384 (MOE_ERR_UNSUPPORTED); M below 2^22. */
+moe_status moe_residual_norm(moe_dtype dtype, const void* h, const void* y, const moe_norm_spec* norm, int32_t M,
+                             int32_t H, void* h_out, void* x, void* stream);
+
+/* Bytes of workspace moe_residual_norm_backward needs (0 for M = 0). */
+size_t moe_residual_norm_workspace_size(int32_t M, int32_t H);
+
+/* Gradients of moe_residual_norm:
+ *  h_out   its h_out (h where y was NULL), dh_out the gradient of it (NULL: 0),
+ *          dx the gradient of x (NULL exactly when pre_weight is)
+ *  dh, dy  gradients of h and y (dy NULL exactly when y is), [M][H] in dtype
+ *  dpost_weight, dpre_weight   device float32 [H]; dgate device float32 [H], or
+ *          [M] per token; each NULL to skip, and must be NULL where the weight
+ *          is.  Sums over rows in float32, in a fixed order; with M = 0 the ones
+ *          over rows become zeros.
+ *  workspace  device, 256-byte aligned; its contents on entry do not matter.
+ * dh and dy may each be one of the inputs; they differ from each other. */
+moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const void* dh_out, const void* dx,
+                                      const void* y, const moe_norm_spec* norm, int32_t M, int32_t H, void* dh, void* dy,
+                                      float* dpost_weight, float* dgate, float* dpre_weight, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Gradient of moe_grouped_gemm's rows (MOE_BF16; all device bfloat16):
+ *   da[p] = W[e]^T dc[p],  dc [P][N] in pair order, e the expert of pair p.
+ *  kind = MOE_GEMM_GATE_UP: w = W1 [E][N=2I][K=H], dc = dz, z NULL, act NULL,
+ *         da [P][K] (summed over a token's pairs by moe_permute_backward).
+ *  kind = MOE_GEMM_DOWN: w = W2 [E][N=H][K=I], dc = dy.  z NULL: da [P][K].
+ *         z [P][2K] (MOE_GEMM_GATE_UP's): the gradient goes on through
+ *         SiLU-and-mul in float32 and da = dz [P][2K], gate columns first; act
+ *         non-NULL then receives silu(gate) * up [P][K] of the same z.
+ * Only rows of pairs with an expert are written.  al, block_m (64 or 128): as
+ * for moe_grouped_gemm.  Errors as there; one expert's weights of 4 GiB less
+ * 64 KiB or more -> MOE_ERR_UNSUPPORTED. */
+moe_status moe_grouped_gemm_dx(moe_gemm_kind kind, moe_dtype dtype, const void* dc, const void* w, const void* z,
+                               const moe_align_bufs* al, int32_t M, int32_t topk, int32_t E, int32_t N, int32_t K,
+                               int32_t block_m, void* da, void* act, void* stream);
+
+/* Gradient of moe_grouped_gemm's weights (MOE_BF16):
+ *   dw[e][n][k] = sum over the pairs p of expert e of dc[p][n] * a[r][k], float32 sums
+ *  kind = MOE_GEMM_GATE_UP: a = x [M][K], r the token of p; MOE_GEMM_DOWN: a = act
+ *  [P][K], r = p.  dc [P][N].  dc and a bfloat16; dw device [E][N][K] in
+ *  dw_dtype, MOE_BF16 or MOE_F32, written in full (zeros for an expert without
+ *  pairs, and with M = 0).  Any block_m of moe_align. */
+moe_status moe_grouped_gemm_dw(moe_gemm_kind kind, moe_dtype dtype, const void* dc, const void* a,
+                               const moe_align_bufs* al, int32_t M, int32_t topk, int32_t E, int32_t N, int32_t K,
+                               int32_t block_m, moe_dtype dw_dtype, void* dw, void* stream);
 
 /* ---------------------------------------------------------- expert streaming
  * The MoE inference post's second design (FusedMoE vs MegaMoE, sections

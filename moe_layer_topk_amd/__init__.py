@@ -15,6 +15,12 @@ float8_e4m3fn with float32 scales [E, N/128, K/128], one per 128 x 128 block;
 -> moe_grouped_gemm with the E4M3 kinds, or the fused layers from bfloat16
 hidden states.  moe_route_grouped / fused_moe_grouped route with a Routing
 (softmax or sigmoid scores, balance bias, expert groups).
+
+Around the experts: moe_permute / moe_unpermute (token rows in expert order and
+back, with weights) and moe_residual_norm (norm after a block, gate, residual
+sum, norm before the next).  For training: their backward calls, moe_grouped_gemm
+with MOE_GEMM_GATE_UP (gate and up before SiLU-and-mul), moe_grouped_gemm_dx and
+moe_grouped_gemm_dw.
 """
 from __future__ import annotations
 
@@ -32,6 +38,7 @@ from ._lib import (  # noqa: F401
     MOE_FP8_E4M3,
     MOE_GEMM_DOWN,
     MOE_GEMM_DOWN_E4M3_ACT,
+    MOE_GEMM_GATE_UP,
     MOE_GEMM_GATE_UP_SILU,
     MOE_GEMM_GATE_UP_SILU_E4M3,
     MOE_SCORE_SIGMOID,
@@ -39,6 +46,7 @@ from ._lib import (  # noqa: F401
     AlignBufs,
     ExpertWeights,
     MoeError,
+    NormSpec,
     RoutingArgs,
     check,
     lib,
@@ -218,11 +226,14 @@ def align_struct(al: dict) -> AlignBufs:
 
 def moe_grouped_gemm(kind: int, a: torch.Tensor, w: torch.Tensor, al: dict, M: int, topk: int,
                      a_scale=None, w_scale=None, c=None, c_amax=None):
-    """GATE_UP: act[P, N/2] = silu(gate) * up;  DOWN: y[P, N].  Returns (c, c_amax)."""
+    """GATE_UP_SILU: act[P, N/2] = silu(gate) * up;  DOWN: y[P, N];  GATE_UP (bfloat16):
+    z[P, N], gate and up before SiLU-and-mul.  Returns (c, c_amax)."""
     E, N, K = w.shape
     dt = _layer_dtype(w, w_scale)
     if dt == MOE_FP8_BLOCK:
         return _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_amax)
+    if kind == MOE_GEMM_GATE_UP:
+        return _gate_up_gemm(a, w, al, M, topk, c), None
     if dt == MOE_W4A16:
         K *= 2  # two 4-bit codes per byte
     P = M * topk
@@ -271,6 +282,336 @@ def _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_scale):
     _call(lib().moe_grouped_gemm, "moe_grouped_gemm", dev, kind, MOE_FP8_BLOCK, _p(a), _p(a_scale), _p(w), _p(w_scale),
           ctypes.byref(bufs), M, topk, E, N, K, block_m, _p(c), _p(c_scale), stream)
     return c, c_scale
+
+
+def _check_align(al: dict, P: int, E: int, dev, block_m=None) -> None:
+    """An alignment (moe_align) of P pairs over E experts on this device."""
+    if al["pairs"] != P or al["expert_counts"].numel() != E or al["sorted_ids"].device != dev:
+        raise ValueError("the alignment (moe_align) is of another batch, number of experts or device")
+    if block_m is not None and al["block_m"] not in block_m:
+        raise ValueError(f"the alignment has block_m {al['block_m']}, expected {' or '.join(map(str, block_m))}")
+
+
+_BF16 = (torch.bfloat16,)
+_ROWS = (torch.float32, torch.bfloat16)
+_GRAD_KINDS = (MOE_GEMM_GATE_UP, MOE_GEMM_DOWN)
+
+
+def _gate_up_gemm(x, w, al, M, topk, z):
+    """moe_grouped_gemm's GATE_UP kind."""
+    E, N, K = w.shape
+    P, dev = M * topk, w.device
+    stream = _stream(w)
+    _need("w", w, _BF16, (E, N, K), dev)
+    _need("a", x, _BF16, (M, K), dev)
+    if z is None:
+        z = torch.empty((P, N), dtype=torch.bfloat16, device=dev)
+    _need("c", z, _BF16, (P, N), dev)
+    _check_align(al, P, E, dev, (64, 128))
+    bufs = align_struct(al)
+    _call(lib().moe_grouped_gemm, "moe_grouped_gemm", dev, MOE_GEMM_GATE_UP, MOE_BF16, _p(x), None, _p(w), None,
+          ctypes.byref(bufs), M, topk, E, N, K, al["block_m"], _p(z), None, stream)
+    return z
+
+
+def moe_grouped_gemm_dx(kind: int, dc: torch.Tensor, w: torch.Tensor, al: dict, M: int, topk: int, z=None, da=None,
+                        act=None):
+    """Gradient of the rows of a grouped product (bfloat16): da[p] = w[e]^T dc[p].
+    kind MOE_GEMM_GATE_UP: dc = dz [P, 2I], w = w1, da [P, H].  MOE_GEMM_DOWN: dc =
+    dy [P, H], w = w2, da [P, I], or with z (moe_grouped_gemm's GATE_UP) the
+    gradient dz [P, 2I] before SiLU-and-mul, and act = silu(gate) * up [P, I].
+    Returns (da, act or None)."""
+    E, N, K = w.shape
+    P, dev = M * topk, w.device
+    stream = _stream(w)
+    if kind not in _GRAD_KINDS:
+        raise ValueError("kind is MOE_GEMM_GATE_UP or MOE_GEMM_DOWN")
+    _need("w", w, _BF16, (E, N, K), dev)
+    _need("dc", dc, _BF16, (P, N), dev)
+    cols = K
+    if z is not None:
+        if kind != MOE_GEMM_DOWN:
+            raise ValueError("z goes with MOE_GEMM_DOWN")
+        cols = 2 * K
+        _need("z", z, _BF16, (P, cols), dev)
+        if act is None:
+            act = torch.empty((P, K), dtype=torch.bfloat16, device=dev)
+        _need("act", act, _BF16, (P, K), dev)
+    elif act is not None:
+        raise ValueError("act is recomputed from z: it needs z")
+    if da is None:
+        da = torch.empty((P, cols), dtype=torch.bfloat16, device=dev)
+    _need("da", da, _BF16, (P, cols), dev)
+    _check_align(al, P, E, dev, (64, 128))
+    bufs = align_struct(al)
+    _call(lib().moe_grouped_gemm_dx, "moe_grouped_gemm_dx", dev, kind, MOE_BF16, _p(dc), _p(w), _p(z), ctypes.byref(bufs),
+          M, topk, E, N, K, al["block_m"], _p(da), _p(act), stream)
+    return da, act
+
+
+def moe_grouped_gemm_dw(kind: int, dc: torch.Tensor, a: torch.Tensor, al: dict, M: int, topk: int, dtype=None, dw=None):
+    """Gradient of the weights of a grouped product, [E, N, K] in dtype (bfloat16 or
+    float32; bfloat16 if neither dtype nor dw is given): the sum over each expert's
+    pairs of dc[p] (outer) a.  kind MOE_GEMM_GATE_UP: dc = dz [P, 2I], a = x [M, H];
+    MOE_GEMM_DOWN: dc = dy [P, H], a = act [P, I]."""
+    P, N = dc.shape
+    K = a.shape[1]
+    E, dev = al["expert_counts"].numel(), dc.device
+    stream = _stream(dc)
+    if kind not in _GRAD_KINDS:
+        raise ValueError("kind is MOE_GEMM_GATE_UP or MOE_GEMM_DOWN")
+    _need("dc", dc, _BF16, (M * topk, N), dev)
+    _need("a", a, _BF16, (M if kind == MOE_GEMM_GATE_UP else M * topk, K), dev)
+    if dw is None:
+        dw = torch.empty((E, N, K), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    _need("dw", dw, _ROWS if dtype is None else (dtype,), (E, N, K), dev)
+    if dw.dtype not in _ROWS:
+        raise ValueError(f"dw is {dw.dtype}, expected torch.float32 or torch.bfloat16")
+    _check_align(al, M * topk, E, dev)
+    bufs = align_struct(al)
+    _call(lib().moe_grouped_gemm_dw, "moe_grouped_gemm_dw", dev, kind, MOE_BF16, _p(dc), _p(a), ctypes.byref(bufs), M, topk,
+          E, N, K, al["block_m"], _DTYPES[dw.dtype], _p(dw), stream)
+    return dw
+
+
+def _row_weights(weights, M, topk, dev) -> None:
+    if weights is not None:
+        _need("weights", weights, _F32, (M, topk), dev)
+
+
+def _rows_shape(name, rows, pair_row, weights, topk):
+    """(topk, M, number of rows, H) of expert rows in the order pair_row says
+    (None: pair order, whose topk comes from the weights or the argument)."""
+    nrows, H = rows.shape
+    if pair_row is not None:
+        M, k = pair_row.shape
+        _need("pair_row", pair_row, (torch.int32,), (M, k), rows.device)
+    else:
+        k = weights.shape[1] if weights is not None else topk
+        if k is None or k < 1:
+            raise ValueError("topk is missing (no pair_row and no weights say it)")
+        if nrows % k:
+            raise ValueError(f"{name} has {nrows} rows in pair order, not a multiple of {k}")
+        M = nrows // k
+    if topk is not None and topk != k:
+        raise ValueError(f"topk is {topk}, expected {k}")
+    _need(name, rows, _ROWS, (nrows, H), rows.device)
+    _row_weights(weights, M, k, rows.device)
+    return k, M, nrows, H
+
+
+def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, al: dict, weights=None, rows=None, pair_row=None):
+    """Token rows [M, H] (float32 or bfloat16) in expert order: rows[r] = w_p x[p // k]
+    for the pair p = al["sorted_ids"][r], zeros in the padding of the experts' runs
+    (rows past the padded total are left as they were).  weights: float32 [M, k] or
+    None.  Returns (rows, pair_row int32 [M, k]: the row of each pair, -1 for an id
+    that is no expert)."""
+    M, H = x.shape
+    topk = topk_ids.shape[1]
+    dev = x.device
+    stream = _stream(x)
+    E, cap = al["expert_counts"].numel(), moe_align_capacity(M, topk, al["expert_counts"].numel(), al["block_m"])
+    _need("x", x, _ROWS, (M, H), dev)
+    _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
+    _row_weights(weights, M, topk, dev)
+    _check_align(al, M * topk, E, dev)
+    if rows is None:
+        rows = torch.empty((cap, H), dtype=x.dtype, device=dev)
+    if pair_row is None:
+        pair_row = torch.empty((M, topk), dtype=torch.int32, device=dev)
+    _need("rows", rows, (x.dtype,), (cap, H), dev)
+    _need("pair_row", pair_row, (torch.int32,), (M, topk), dev)
+    bufs = align_struct(al)
+    _call(lib().moe_permute, "moe_permute", dev, _DTYPES[x.dtype], x.data_ptr(), _p(weights), topk_ids.data_ptr(),
+          ctypes.byref(bufs), M, topk, E, al["block_m"], H, rows.data_ptr(), pair_row.data_ptr(), stream)
+    return rows, pair_row
+
+
+def moe_unpermute(rows: torch.Tensor, pair_row=None, weights=None, topk=None, out_dtype=None, out=None):
+    """Expert rows back to token order: out[t] = sum_j w_tj rows[pair_row[t, j]]
+    (weights None: 1; pairs without a row add nothing; pair_row None: rows in pair
+    order, with topk where no weights say it)."""
+    dev = rows.device
+    stream = _stream(rows)
+    k, M, nrows, H = _rows_shape("rows", rows, pair_row, weights, topk)
+    if out is None:
+        out = torch.empty((M, H), dtype=rows.dtype if out_dtype is None else out_dtype, device=dev)
+    _need("out", out, _ROWS if out_dtype is None else (out_dtype,), (M, H), dev)
+    _call(lib().moe_unpermute, "moe_unpermute", dev, _DTYPES[rows.dtype], rows.data_ptr(), nrows, _p(pair_row), _p(weights),
+          M, k, H, moe_dtype(out), out.data_ptr(), stream)
+    return out
+
+
+def moe_unpermute_backward(dout: torch.Tensor, rows, weights, pair_row=None, al=None, topk=None, nrows=None, drows=None,
+                           dweights=None):
+    """Gradients of moe_unpermute (pair_row None: of moe_combine) for dout [M, H]:
+    drows[r] = w_p dout[p // k] and dweights [M, k], dweights[p] = <rows[r], dout[p // k]>.
+    rows None: no gradient of the weights (then nrows says how many rows there are
+    when neither pair order nor al does).  al: the alignment the rows follow; the
+    padding rows of its runs become zeros.  drows may be rows.  Returns (drows,
+    dweights or None)."""
+    M, H = dout.shape
+    dev = dout.device
+    stream = _stream(dout)
+    if pair_row is not None:
+        k = pair_row.shape[1]
+        _need("pair_row", pair_row, (torch.int32,), (M, k), dev)
+    else:
+        k = weights.shape[1] if weights is not None else topk
+        if k is None or k < 1:
+            raise ValueError("topk is missing (no pair_row and no weights say it)")
+    if topk is not None and topk != k:
+        raise ValueError(f"topk is {topk}, expected {k}")
+    E = block_m = 0
+    bufs = None
+    have = [t.shape[0] for t in (rows, drows) if t is not None] + ([nrows] if nrows is not None else [])
+    if al is not None:
+        E, block_m = al["expert_counts"].numel(), al["block_m"]
+        if pair_row is None:
+            raise ValueError("al goes with pair_row (rows in pair order have no padding)")
+        _check_align(al, M * k, E, dev)
+        bufs = ctypes.byref(align_struct(al))
+        have.append(moe_align_capacity(M, k, E, block_m))
+    if pair_row is None:
+        have.append(M * k)
+    if not have:
+        raise ValueError("the number of rows is missing: rows, drows, al or nrows")
+    n = have[0]
+    _need("dout", dout, _ROWS, (M, H), dev)
+    _row_weights(weights, M, k, dev)
+    if rows is not None:
+        if weights is None:
+            raise ValueError("a gradient of the weights needs weights")
+        _need("rows", rows, (dout.dtype,), (n, H), dev)
+        if dweights is None:
+            dweights = torch.empty((M, k), dtype=torch.float32, device=dev)
+        _need("dweights", dweights, _F32, (M, k), dev)
+    elif dweights is not None:
+        raise ValueError("a gradient of the weights needs rows")
+    if drows is None:
+        drows = torch.empty((n, H), dtype=dout.dtype, device=dev)
+    _need("drows", drows, (dout.dtype,), (n, H), dev)
+    if any(v != n for v in have):
+        raise ValueError(f"rows, drows, al and nrows disagree on the number of rows: {have}")
+    _call(lib().moe_unpermute_backward, "moe_unpermute_backward", dev, _DTYPES[dout.dtype], dout.data_ptr(), _p(rows), n,
+          _p(pair_row), _p(weights), bufs, M, k, E, block_m, H, drows.data_ptr(), _p(dweights), stream)
+    return drows, dweights
+
+
+def moe_permute_backward(drows: torch.Tensor, pair_row=None, x=None, weights=None, topk=None, dx=None, dweights=None):
+    """Gradients of moe_permute for drows: dx[t] = sum_j w_tj drows[pair_row[t, j]], and
+    with x (and weights) dweights[p] = <drows[r], x[p // k]>.  pair_row None: rows in
+    pair order (moe_grouped_gemm_dx).  Returns (dx, dweights or None)."""
+    dev = drows.device
+    stream = _stream(drows)
+    k, M, nrows, H = _rows_shape("drows", drows, pair_row, weights, topk)
+    if x is not None:
+        if weights is None:
+            raise ValueError("a gradient of the weights needs weights")
+        _need("x", x, (drows.dtype,), (M, H), dev)
+        if dweights is None:
+            dweights = torch.empty((M, k), dtype=torch.float32, device=dev)
+        _need("dweights", dweights, _F32, (M, k), dev)
+    elif dweights is not None:
+        raise ValueError("a gradient of the weights needs x")
+    if dx is None:
+        dx = torch.empty((M, H), dtype=drows.dtype, device=dev)
+    _need("dx", dx, (drows.dtype,), (M, H), dev)
+    _call(lib().moe_permute_backward, "moe_permute_backward", dev, _DTYPES[drows.dtype], drows.data_ptr(), nrows,
+          _p(pair_row), _p(x), _p(weights), M, k, H, dx.data_ptr(), _p(dweights), stream)
+    return dx, dweights
+
+
+def _norm_spec(h, y, post_weight, gate, scale, pre_weight, eps):
+    """(moe_norm_spec, gate of [M, 1]) for rows h [M, H], its weights checked."""
+    M, H = h.shape
+    dev = h.device
+    _need("h", h, _ROWS, (M, H), dev)
+    if y is not None:
+        _need("y", y, (h.dtype,), (M, H), dev)
+    elif post_weight is not None or gate is not None:
+        raise ValueError("post_weight and gate are a block's: they need y")
+    given = [t for t in (post_weight, gate, pre_weight) if t is not None]
+    wdt = given[0].dtype if given else h.dtype
+    if wdt not in _ROWS:
+        raise ValueError(f"the norms' weights are {wdt}, expected torch.float32 or torch.bfloat16")
+    per_token = gate is not None and gate.dim() == 2
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            _need(name, t, (wdt,), (H,), dev)
+    if gate is not None:
+        _need("gate", gate, (wdt,), (M, 1) if per_token else (H,), dev)
+    return NormSpec(*(None if t is None else t.data_ptr() for t in (post_weight, gate, pre_weight)), _DTYPES[wdt],
+                    int(per_token), scale, eps), per_token
+
+
+def moe_residual_norm(h: torch.Tensor, y=None, post_weight=None, gate=None, scale: float = 1.0, pre_weight=None,
+                      eps: float = 1e-6, h_out=None, x=None):
+    """One pass over the rows [M, H] between two blocks: with u = norm(y) * post_weight
+    (y without a post_weight), h_out = h + scale * gate * u, x = norm(h_out) * pre_weight,
+    norm(v) = v / sqrt(mean(v^2) + eps).  gate: [H], or [M, 1] for one a token.  The
+    weights are float32 or bfloat16, all alike.  Without y: x = norm(h) * pre_weight
+    and h_out is h.  h_out and x may be h or y.  Returns (h_out, x or None)."""
+    dev = h.device
+    stream = _stream(h)
+    spec, _ = _norm_spec(h, y, post_weight, gate, scale, pre_weight, eps)
+    M, H = h.shape
+    if y is None and pre_weight is None:
+        raise ValueError("nothing to do: neither y nor pre_weight")
+    if y is None and h_out is not None:
+        raise ValueError("without y, h_out is h")
+    if pre_weight is None and x is not None:
+        raise ValueError("x needs pre_weight")
+    if y is not None and h_out is None:
+        h_out = torch.empty_like(h)
+    if pre_weight is not None and x is None:
+        x = torch.empty_like(h)
+    for name, t in (("h_out", h_out), ("x", x)):
+        if t is not None:
+            _need(name, t, (h.dtype,), (M, H), dev)
+    _call(lib().moe_residual_norm, "moe_residual_norm", dev, _DTYPES[h.dtype], h.data_ptr(), _p(y), ctypes.byref(spec), M,
+          H, _p(h_out), _p(x), stream)
+    return (h if y is None else h_out), x
+
+
+def moe_residual_norm_backward(h_out: torch.Tensor, dh_out=None, dx=None, y=None, post_weight=None, gate=None,
+                               scale: float = 1.0, pre_weight=None, eps: float = 1e-6, dh=None, dy=None, workspace=None):
+    """Gradients of moe_residual_norm for dh_out (None: zero) and dx, from its h_out (h
+    where it had no y), y and weights.  dh and dy may be inputs.  Returns (dh, dy,
+    dpost_weight, dgate, dpre_weight): rows in their own type, weights' in float32,
+    None for what was not there."""
+    dev = h_out.device
+    stream = _stream(h_out)
+    spec, per_token = _norm_spec(h_out, y, post_weight, gate, scale, pre_weight, eps)
+    M, H = h_out.shape
+    if (dx is None) != (pre_weight is None):
+        raise ValueError("dx and pre_weight go together")
+    for name, t in (("dh_out", dh_out), ("dx", dx)):
+        if t is not None:
+            _need(name, t, (h_out.dtype,), (M, H), dev)
+    if dh is None:
+        dh = torch.empty_like(h_out)
+    _need("dh", dh, (h_out.dtype,), (M, H), dev)
+    if y is None and dy is not None:
+        raise ValueError("dy needs y")
+    if y is not None:
+        if dy is None:
+            dy = torch.empty_like(y)
+        _need("dy", dy, (h_out.dtype,), (M, H), dev)
+
+    def sums(w, shape):
+        return None if w is None else torch.empty(shape, dtype=torch.float32, device=dev)
+
+    dpost, dgate, dpre = sums(post_weight, H), sums(gate, (M, 1) if per_token else H), sums(pre_weight, H)
+    need = lib().moe_residual_norm_workspace_size(M, H)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace is {workspace.dtype} on {workspace.device}, expected contiguous torch.uint8 on {dev}")
+    _call(lib().moe_residual_norm_backward, "moe_residual_norm_backward", dev, _DTYPES[h_out.dtype], h_out.data_ptr(),
+          _p(dh_out), _p(dx), _p(y), ctypes.byref(spec), M, H, dh.data_ptr(), _p(dy), _p(dpost), _p(dgate), _p(dpre),
+          _p(workspace), workspace.numel(), stream)
+    return dh, dy, dpost, dgate, dpre
 
 
 def moe_quant_block(x: torch.Tensor, block_rows: int = 1, q=None, scale=None):

@@ -10,7 +10,7 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 (MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_ALIGNMENT, MOE_ERR_HIP,
  MOE_ERR_SCRATCH) = range(8)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_W4A16, MOE_FP8_BLOCK = 0, 1, 2, 3, 4
-MOE_GEMM_GATE_UP_SILU, MOE_GEMM_DOWN, MOE_GEMM_DOWN_E4M3_ACT, MOE_GEMM_GATE_UP_SILU_E4M3 = 0, 1, 2, 3
+MOE_GEMM_GATE_UP_SILU, MOE_GEMM_DOWN, MOE_GEMM_DOWN_E4M3_ACT, MOE_GEMM_GATE_UP_SILU_E4M3, MOE_GEMM_GATE_UP = range(5)
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
@@ -28,6 +28,13 @@ class RoutingArgs(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class NormSpec(ctypes.Structure):
+    """moe_norm_spec"""
+    _fields_ = [("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("w_dtype", ctypes.c_int), ("gate_per_token", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -68,6 +75,20 @@ SIGNATURES = {
     "moe_cache_prefetch": (ctypes.c_int, [_P, _P, _I32]),
     "moe_cache_stats": (ctypes.c_int, [_P, _P, _P, _P, _P]),
     "fused_moe_cached": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_permute": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, ctypes.POINTER(AlignBufs), _I32, _I32, _I32, _I32, _I32, _P,
+                                   _P, _P]),
+    "moe_unpermute": (ctypes.c_int, [ctypes.c_int, _P, _I64, _P, _P, _I32, _I32, _I32, ctypes.c_int, _P, _P]),
+    "moe_unpermute_backward": (ctypes.c_int, [ctypes.c_int, _P, _P, _I64, _P, _P, ctypes.POINTER(AlignBufs), _I32, _I32,
+                                              _I32, _I32, _I32, _P, _P, _P]),
+    "moe_permute_backward": (ctypes.c_int, [ctypes.c_int, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_residual_norm": (ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.POINTER(NormSpec), _I32, _I32, _P, _P, _P]),
+    "moe_residual_norm_workspace_size": (_SZ, [_I32, _I32]),
+    "moe_residual_norm_backward": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, _P, ctypes.POINTER(NormSpec), _I32, _I32, _P,
+                                                  _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_grouped_gemm_dx": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P, _P, ctypes.POINTER(AlignBufs), _I32, _I32,
+                                           _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_grouped_gemm_dw": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P, ctypes.POINTER(AlignBufs), _I32, _I32,
+                                           _I32, _I32, _I32, _I32, ctypes.c_int, _P, _P]),
     "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

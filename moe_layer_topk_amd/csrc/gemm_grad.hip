@@ -1,0 +1,436 @@
+// Gradients of the grouped expert products, bfloat16 operands, float32 sums:
+//
+//   dx:  da[p][k]    = sum_n dc[p][n] W[e][n][k]            (rows of expert e)
+//        through SiLU-and-mul, with (g, u) the kept products z[p] and d = da[p]:
+//        dg = d u s (1 + g (1 - s)),  du = d g s,  act = g s u,  s = 1 / (1 + exp(-g))
+//   dw:  dW[e][n][k] = sum_{p of e} dc[p][n] a[p][k]
+//
+// The weights are stored with k contiguous, so dx sums over the rows of W and dw
+// over the rows of both operands: what a lane of the matrix instruction wants next
+// to each other (eight terms of the sum) lies a row apart.  The tiles therefore go
+// to LDS as they lie in memory, by direct copies, and are transposed on the way to
+// the registers (ds_read_b64_tr_b16: 16 lanes read four rows of 16 columns and each
+// gets a column's four values).
+#include <type_traits>
+
+#include "moe_device.h"
+#include "moe_launch.h"
+#include "moe_tile.h"
+#include "moe_train.h"
+
+namespace moe {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kXcds = 8;
+
+// What rows and columns outside a matrix read.
+__device__ uint4 grad_zeros[64];
+
+// Rows of 256 columns (512 bytes) in LDS.  The 32-byte piece q of row r lies at
+// place q ^ 2 (r mod 4): the 32 lanes that read four rows at two neighbouring
+// pieces meet every bank once.
+__device__ __forceinline__ int tr_place(int q, int r) { return q ^ ((r & 3) << 1); }
+
+// Eight consecutive rows (terms of the sum) of a column, from LDS byte address
+// `at` (the lane's, see tr_lane) and the next four rows.
+__device__ __forceinline__ bf16x8 tr_read8(unsigned at) {
+    struct Two {
+        s16x4 lo, hi;
+    } v;
+    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at);
+    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(at + 4 * 512));
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// The lane's address in a tile at 0 for columns col0 .. col0 + 31 (a multiple of
+// 32) and rows 0 .. 15: lanes 0-15 and 16-31 take columns 0-15 and 16-31 of rows
+// 0-7, lanes 32-63 the same of rows 8-15.
+__device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
+    const int g = lane >> 4, i = lane & 15;
+    const int r = 8 * (g >> 1) + (i >> 2), q = col0 / 16 + (g & 1);
+    return (unsigned)(r * 512 + tr_place(q, r) * 32 + (i & 3) * 8);
+}
+
+// ------------------------------------------------------------------------ dx
+//
+// Block tile BM rows (of one expert's run) x 256 columns k, 64 terms n a stage in
+// a ring of three; four wavefronts of BM/2 x 128.  W's columns are the matrix
+// instruction's rows, so a lane ends up with four consecutive k of a token.
+
+template <int BM>
+struct DxCfg {
+    static constexpr int ST = 3, Threads = 256;
+    static constexpr int ABytes = BM * 128, WBytes = 64 * 512, StageBytes = ABytes + WBytes;
+    static constexpr int ALoads = BM / 8 / 4, WLoads = 8, L = ALoads + WLoads;  // copies a wave and stage
+    static constexpr int TM = BM / 64, TN = 4;
+    static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + BM * 4;
+    // chunk c of 16 bytes of row r (rows of 128 bytes)
+    __device__ static __forceinline__ int swz(int c, int r) { return c ^ ((r >> 1) & 7); }
+};
+
+template <int BM, bool SILU>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2)))
+grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
+    using C = DxCfg<BM>;
+    extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
+    const int nb = m_tiles * k_tiles;
+    const int per = (nb + kXcds - 1) / kXcds;
+    const int t = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+    if (t >= nb) return;
+    // groups of `group` weight tiles; inside a group the row tiles advance slowest
+    const int ng = t / (group * m_tiles);
+    const int gw = min(group, k_tiles - ng * group);
+    const int rem = t - ng * group * m_tiles;
+    const int mtile = rem / gw, ktile = ng * group + rem % gw;
+    const int e = g.al.tile_expert[mtile];
+    if (e < 0) return;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int N = g.N, K = g.K, P = g.M * g.topk;
+    const int k0 = ktile * 256;
+    const int32_t* sorted = g.al.sorted_ids + (size_t)mtile * BM;
+    int* ids_s = reinterpret_cast<int*>(grad_lds + C::IdsOffset);
+    for (int i = tid; i < BM; i += C::Threads) ids_s[i] = sorted[i];
+
+    // sources of this wave's copies: rows of dc, and rows n of W (512 of their bytes)
+    const char* asrc[C::ALoads];
+#pragma unroll
+    for (int j = 0; j < C::ALoads; ++j) {
+        const int r = (wave * C::ALoads + j) * 8 + (lane >> 3);
+        int p = sorted[r];
+        if ((unsigned)p >= (unsigned)P) p = sorted[0];  // padding: any row, its results are dropped
+        asrc[j] = static_cast<const char*>(g.dc) + (size_t)p * N * 2 + C::swz(lane & 7, r) * 16;
+    }
+    // (columns past K read the next row, past the last row zeros; they are dropped)
+    const v4i_rsrc wrsrc = buf_rsrc(static_cast<const char*>(g.w) + (size_t)e * N * K * 2, (unsigned)((size_t)N * K * 2));
+    unsigned wsrc[C::WLoads];
+#pragma unroll
+    for (int j = 0; j < C::WLoads; ++j) {
+        const int r = (wave * C::WLoads + j) * 2 + (lane >> 5), c = lane & 31;
+        wsrc[j] = (unsigned)(((size_t)r * K + k0) * 2) + (tr_place(c >> 1, r) * 2 + (c & 1)) * 16;
+    }
+    const unsigned lds0 = lds_addr_of(grad_lds);
+    auto issue_part = [&](int kt, int j0, int j1) {
+        const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+#pragma unroll
+        for (int j = 0; j < C::L; ++j) {
+            if (j < j0 || j >= j1) continue;
+            if (j < C::ALoads)
+                lds_dma16_at(asrc[j] + (size_t)kt * 128, st + (wave * C::ALoads + j) * 1024);
+            else
+                lds_dma16_buf(wrsrc, wsrc[j - C::ALoads], (unsigned)((size_t)kt * 128 * K),
+                              st + C::ABytes + (wave * C::WLoads + (j - C::ALoads)) * 1024);
+        }
+    };
+
+    f32x16 acc[C::TM][C::TN];
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    int arow[C::TM];
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) arow[i] = wm * (BM / 2) + 32 * i + (lane & 31);
+    unsigned wlane[C::TN];
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) wlane[j] = C::ABytes + tr_lane(lane, wn * 128 + 32 * j);
+    // 32-row groups of the tile that hold no pair are left out
+    const int nreal = min(BM, g.al.expert_offsets[e] + g.al.expert_counts[e] - mtile * BM);
+    const int live = __builtin_amdgcn_readfirstlane(min(C::TM, max(0, (nreal - wm * (BM / 2) + 31) / 32)));
+
+    const int nk = N / 64;
+#pragma unroll
+    for (int s0 = 0; s0 < C::ST - 1; ++s0)
+        if (s0 < nk) issue_part(s0, 0, C::L);
+    auto stage = [&](int kt, auto pf_tag, auto lt_tag) {
+        constexpr bool pf = decltype(pf_tag)::value;
+        constexpr int LT = decltype(lt_tag)::value;
+        if constexpr (pf)
+            wait_vm<(C::ST - 2) * C::L>();
+        else
+            wait_vm_runtime<C::L>(min(C::ST - 2, nk - 1 - kt));
+        __syncthreads();
+        const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+        const char* sa = grad_lds + (kt % C::ST) * C::StageBytes;
+        bf16x8 af[2][C::TM], wf[2][C::TN];
+        auto read_frags = [&](int buf, int ks) {
+            const int c = ks * 2 + (lane >> 5);
+#pragma unroll
+            for (int i = 0; i < LT; ++i)
+                af[buf][i] = *reinterpret_cast<const bf16x8*>(sa + arow[i] * 128 + (C::swz(c, arow[i]) << 4));
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j)
+                if (LT) wf[buf][j] = tr_read8(st + wlane[j] + ks * 16 * 512);
+        };
+        read_frags(0, 0);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const int cur = ks & 1;
+            if (ks < 3) read_frags(cur ^ 1, ks + 1);
+            // this substep's share of the next copies, between the products
+            const int j0 = ks * C::L / 4, j1 = (ks + 1) * C::L / 4;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < C::TM * C::TN; ++q) {
+                const int i = q / C::TN, j = q % C::TN;
+                if (i < LT) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[cur][j], af[cur][i], acc[i][j], 0, 0, 0);
+                if (pf && (q & 1) && j0 + q / 2 < j1) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    issue_part(kt + C::ST - 1, j0 + q / 2, j0 + q / 2 + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if (pf && C::TM * C::TN / 2 < j1 - j0) issue_part(kt + C::ST - 1, j0 + C::TM * C::TN / 2, j1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const int nmain = nk - (C::ST - 1) > 0 ? nk - (C::ST - 1) : 0;
+    auto kloop = [&](auto lt) {
+        for (int kt = 0; kt < nmain; ++kt) stage(kt, std::true_type{}, lt);
+        for (int kt = nmain; kt < nk; ++kt) stage(kt, std::false_type{}, lt);
+    };
+    if (live == C::TM)
+        kloop(std::integral_constant<int, C::TM>{});
+    else if (C::TM > 1 && live == 1)
+        kloop(std::integral_constant<int, 1>{});
+    else
+        kloop(std::integral_constant<int, 0>{});
+
+    // ---- epilogue: the wave's tile through LDS (rows of 128 columns, 16 bytes of
+    // padding), so that memory sees whole lines
+    __syncthreads();
+    constexpr int kElem = SILU ? 4 : 2, kRow = 128 * kElem + 16, kRows = BM / 2;
+    static_assert(4 * kRows * kRow <= C::IdsOffset, "epilogue");
+    char* mine = grad_lds + wave * kRows * kRow;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                char* at = mine + (32 * i + (lane & 31)) * kRow + (32 * j + 8 * v + 4 * (lane >> 5)) * kElem;
+                const float x0 = acc[i][j][4 * v], x1 = acc[i][j][4 * v + 1], x2 = acc[i][j][4 * v + 2],
+                            x3 = acc[i][j][4 * v + 3];
+                if constexpr (SILU)
+                    *reinterpret_cast<float4*>(at) = make_float4(x0, x1, x2, x3);
+                else
+                    *reinterpret_cast<uint2*>(at) = uint2{pack_bf2(x0, x1), pack_bf2(x2, x3)};
+            }
+    const int c8 = (lane & 15) * 8, col = k0 + wn * 128 + c8;
+    if (col >= K) return;
+    const int rows = min(kRows, nreal - wm * kRows);
+    for (int r = lane >> 4; r < rows; r += 4) {
+        const size_t p = (size_t)ids_s[wm * kRows + r];
+        const char* at = mine + r * kRow + c8 * kElem;
+        if constexpr (SILU) {
+            const uint16_t* z = static_cast<const uint16_t*>(g.z) + p * 2 * K + col;
+            const uint4 zg = *reinterpret_cast<const uint4*>(z), zu = *reinterpret_cast<const uint4*>(z + K);
+            const float4 d0 = *reinterpret_cast<const float4*>(at), d1 = *reinterpret_cast<const float4*>(at + 16);
+            const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+            const uint32_t ug[4] = {zg.x, zg.y, zg.z, zg.w}, uu[4] = {zu.x, zu.y, zu.z, zu.w};
+            float dg[8], du[8], ac[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float gv = __uint_as_float((i & 1) ? ug[i / 2] & 0xffff0000u : ug[i / 2] << 16);
+                const float uv = __uint_as_float((i & 1) ? uu[i / 2] & 0xffff0000u : uu[i / 2] << 16);
+                const float s = 1.0f / (1.0f + __expf(-gv));
+                const float gs = gv * s;
+                du[i] = d[i] * gs;
+                ac[i] = gs * uv;
+                dg[i] = d[i] * uv * s * (1.0f + gv * (1.0f - s));
+            }
+            uint16_t* o = static_cast<uint16_t*>(g.out) + p * 2 * K + col;
+            *reinterpret_cast<uint4*>(o) = uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])};
+            *reinterpret_cast<uint4*>(o + K) = uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])};
+            if (g.act)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.act) + p * K + col) =
+                    uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])};
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p * K + col) = *reinterpret_cast<const uint4*>(at);
+        }
+    }
+}
+
+template <int BM, bool SILU>
+static hipError_t launch_dx_t(const GradCall& c, hipStream_t s) {
+    using C = DxCfg<BM>;
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dx_kernel<BM, SILU>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::LdsBytes);
+    if (attr != hipSuccess) return attr;
+    const int m_tiles = (int)(moe_align_capacity(c.M, c.topk, c.E, BM) / BM), k_tiles = (c.K + 255) / 256;
+    const int64_t nb = (int64_t)m_tiles * k_tiles;
+    const int group = k_tiles <= 8 ? k_tiles : 2;
+    hipLaunchKernelGGL((grad_dx_kernel<BM, SILU>), dim3((unsigned)((nb + kXcds - 1) / kXcds * kXcds)), dim3(C::Threads),
+                       C::LdsBytes, s, c, m_tiles, k_tiles, group);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_dx(const GradCall& c, hipStream_t s) {
+    if (c.block_m == 128) return c.z ? launch_dx_t<128, true>(c, s) : launch_dx_t<128, false>(c, s);
+    return c.z ? launch_dx_t<64, true>(c, s) : launch_dx_t<64, false>(c, s);
+}
+
+// ------------------------------------------------------------------------ dw
+//
+// Block tile 256 n x 256 k of one expert's matrix, 32 pair rows a stage in a ring
+// of four; eight wavefronts of 64 x 128, two a SIMD.  Both operands are transposed
+// on the way to the registers.  Rows past the expert's last and columns past the
+// matrix read zeros.  Every XCD takes an eighth of each expert's tiles: experts
+// with many rows are shared by all of the chip.
+
+struct DwCfg {
+    static constexpr int ST = 4, Threads = 512, RP = 32;
+    static constexpr int HalfBytes = RP * 512, StageBytes = 2 * HalfBytes;
+    static constexpr int Ids = 4096;  // rows between refills of the id list
+    static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + Ids * 4;
+    static constexpr int L = 4;  // copies a wave and stage: two of dc's rows, two of a's
+};
+
+template <int ODT>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+grad_dw_kernel(GradCall g, int n_tiles, int k_tiles, int per_xcd) {
+    using C = DwCfg;
+    extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
+    const int xcd = blockIdx.x % kXcds, l = blockIdx.x / kXcds;
+    const int e = l / per_xcd, t = xcd * per_xcd + l % per_xcd;
+    if (t >= n_tiles * k_tiles) return;
+    // groups of four k tiles, n tiles in order: what runs together on an XCD covers
+    // a few of each
+    const int gk = t / (n_tiles * 4), gw = min(4, k_tiles - gk * 4), rem = t - gk * n_tiles * 4;
+    const int n0 = (rem / gw) * 256, k0 = (gk * 4 + rem % gw) * 256;
+    const int N = g.N, K = g.K;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave >> 1, wk = wave & 1;
+    const int count = g.al.expert_counts[e];
+    const int32_t* sorted = g.al.sorted_ids + g.al.expert_offsets[e];
+    int* ids_s = reinterpret_cast<int*>(grad_lds + C::IdsOffset);
+
+    // copy j of the wave: rows 4 wave + 2 j and the next of a stage, 32 lanes each
+    const char* zeros = reinterpret_cast<const char*>(grad_zeros);
+    const int c = lane & 31, lrow = 4 * wave + (lane >> 5);
+    int ncol[2], kcol[2];  // the lane's first column of dc and of a (copy j)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int lc = (tr_place(c >> 1, lrow + 2 * j) * 2 + (c & 1)) * 8;
+        ncol[j] = n0 + lc;
+        kcol[j] = k0 + lc;
+    }
+    const unsigned lds0 = lds_addr_of(grad_lds);
+    f32x16 acc[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    unsigned nlane[2], klane[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) nlane[i] = tr_lane(lane, wn * 64 + 32 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) klane[j] = C::HalfBytes + tr_lane(lane, wk * 128 + 32 * j);
+
+    for (int base = 0; base < count; base += C::Ids) {
+        const int n = min(C::Ids, count - base);
+        __syncthreads();
+        for (int i = tid; i < n; i += C::Threads) ids_s[i] = sorted[base + i];
+        __syncthreads();
+        const int nst = (n + C::RP - 1) / C::RP;
+        auto issue = [&](int kt) {
+            const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = kt * C::RP + lrow + 2 * j;
+                const char *pa = zeros + (lane & 31) * 16, *pb = pa;
+                if (r < n) {
+                    const int p = ids_s[r];
+                    if (ncol[j] < N) pa = static_cast<const char*>(g.dc) + ((size_t)p * N + ncol[j]) * 2;
+                    const int q = g.per_token ? p / g.topk : p;
+                    if (kcol[j] < K) pb = static_cast<const char*>(g.a) + ((size_t)q * K + kcol[j]) * 2;
+                }
+                const unsigned at = st + (4 * wave + 2 * j) * 512;
+                lds_dma16_at(pa, at);
+                lds_dma16_at(pb, at + C::HalfBytes);
+            }
+        };
+#pragma unroll
+        for (int s0 = 0; s0 < C::ST - 1; ++s0)
+            if (s0 < nst) issue(s0);
+        for (int kt = 0; kt < nst; ++kt) {
+            const int later = min(C::ST - 2, nst - 1 - kt);  // stages in flight behind this one
+            if (later == 2) wait_vm<2 * C::L>();
+            else if (later == 1) wait_vm<C::L>();
+            else wait_vm<0>();
+            __syncthreads();
+            if (kt + C::ST - 1 < nst) issue(kt + C::ST - 1);
+            const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 nf[2], kf[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) nf[i] = tr_read8(st + nlane[i] + ks * 16 * 512);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kf[j] = tr_read8(st + klane[j] + ks * 16 * 512);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[j], nf[i], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+
+    // ---- epilogue: 32 n rows of the wave's tile at a time through LDS
+    __syncthreads();
+    constexpr int kElem = ODT == MOE_F32 ? 4 : 2, kRow = 128 * kElem + 16;
+    static_assert(8 * 32 * kRow <= C::LdsBytes, "epilogue");
+    char* mine = grad_lds + wave * 32 * kRow;
+    char* out = static_cast<char*>(g.out) + (size_t)e * N * K * kElem;
+    constexpr int kLanes = 128 * kElem / 16;  // of a row
+    const int col = k0 + wk * 128 + (lane % kLanes) * (16 / kElem);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                char* at = mine + (lane & 31) * kRow + (32 * j + 8 * v + 4 * (lane >> 5)) * kElem;
+                const float x0 = acc[i][j][4 * v], x1 = acc[i][j][4 * v + 1], x2 = acc[i][j][4 * v + 2],
+                            x3 = acc[i][j][4 * v + 3];
+                if constexpr (ODT == MOE_F32)
+                    *reinterpret_cast<float4*>(at) = make_float4(x0, x1, x2, x3);
+                else
+                    *reinterpret_cast<uint2*>(at) = uint2{pack_bf2(x0, x1), pack_bf2(x2, x3)};
+            }
+#pragma unroll
+        for (int q = 0; q < 32 * kLanes / 64; ++q) {
+            const int r = q * (64 / kLanes) + lane / kLanes, n = n0 + wn * 64 + 32 * i + r;
+            const uint4 v = *reinterpret_cast<const uint4*>(mine + r * kRow + (lane % kLanes) * 16);
+            if (n < N && col < K) *reinterpret_cast<uint4*>(out + ((size_t)n * K + col) * kElem) = v;
+        }
+    }
+}
+
+template <int ODT>
+static hipError_t launch_dw_t(const GradCall& c, hipStream_t s) {
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dw_kernel<ODT>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, DwCfg::LdsBytes);
+    if (attr != hipSuccess) return attr;
+    const int n_tiles = (c.N + 255) / 256, k_tiles = (c.K + 255) / 256;
+    const int per_xcd = (n_tiles * k_tiles + kXcds - 1) / kXcds;
+    hipLaunchKernelGGL((grad_dw_kernel<ODT>), dim3((unsigned)(kXcds * c.E * per_xcd)), dim3(DwCfg::Threads), DwCfg::LdsBytes,
+                       s, c, n_tiles, k_tiles, per_xcd);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_dw(const GradCall& c, hipStream_t s) {
+    return c.out_dtype == MOE_F32 ? launch_dw_t<MOE_F32>(c, s) : launch_dw_t<MOE_BF16>(c, s);
+}
+
+}  // namespace moe

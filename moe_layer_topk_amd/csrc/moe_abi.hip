@@ -246,8 +246,9 @@ moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, 
                             int32_t topk, int32_t E, int32_t N, int32_t K, int32_t block_m, void* c,
                             float* c_amax, void* stream) {
     if (kind != MOE_GEMM_GATE_UP_SILU && kind != MOE_GEMM_DOWN && kind != MOE_GEMM_DOWN_E4M3_ACT &&
-        kind != MOE_GEMM_GATE_UP_SILU_E4M3)
+        kind != MOE_GEMM_GATE_UP_SILU_E4M3 && kind != MOE_GEMM_GATE_UP)
         return MOE_ERR_UNSUPPORTED;
+    if (kind == MOE_GEMM_GATE_UP && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
     if (!known_dtype(dtype)) return MOE_ERR_UNSUPPORTED;
     if (dtype == MOE_FP8_BLOCK)
         return block_gemm(kind, a, a_scale, w, w_scale, al, M, topk, E, N, K, block_m, c, c_amax,
@@ -259,8 +260,12 @@ moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, 
     moe_status st = check_router(M, E, topk);
     if (st != MOE_OK) return st;
     if (N < 1 || K < 1 || N % 128 || K % 128) return MOE_ERR_SHAPE;
-    if (kind == MOE_GEMM_GATE_UP_SILU && N % 256) return MOE_ERR_SHAPE;
+    if ((kind == MOE_GEMM_GATE_UP_SILU || kind == MOE_GEMM_GATE_UP) && N % 256) return MOE_ERR_SHAPE;
     if (!valid_block_m(block_m)) return MOE_ERR_UNSUPPORTED;
+    // (the tile kernel's rows and 32-bit offsets into its operands)
+    if (kind == MOE_GEMM_GATE_UP &&
+        (!prefill_supported_block_m(block_m) || (uint64_t)M * K * 2 > 0xffffffffull || (uint64_t)N * K * 2 > 0xffffffffull))
+        return MOE_ERR_UNSUPPORTED;
     const bool fp8 = dtype == MOE_FP8_E4M3, w4 = dtype == MOE_W4A16;
     if ((fp8 || w4) && K % 256) return MOE_ERR_SHAPE;
     if (!fp8 && (a_scale || c_amax)) return MOE_ERR_UNSUPPORTED;

@@ -50,6 +50,7 @@ moe_status hip_status(hipError_t e);
 moe_status check_router(int32_t M, int32_t E, int32_t topk);
 moe_status check_routing(const moe_routing* r, int32_t E, int32_t topk);
 
+bool valid_block_m(int32_t b);
 bool known_dtype(moe_dtype d);
 bool scaled_weights(moe_dtype d);  // weights that carry scales
 int dim_multiple(moe_dtype d);     // what H and I must be multiples of

@@ -1,0 +1,90 @@
+// Launchers of what stands around the experts: rows in expert order and back,
+// the norms around a block, and the gradients of the grouped products.
+// Arguments are validated by the caller (train_abi.hip) before any of these run.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+namespace moe {
+
+// Rows of tokens in expert order.  weights NULL: 1.  rows_in non-null: also
+// dots[p] = <rows_in[row of p], src[p / topk]>.  pair_row NULL: the row of pair p
+// is p.  al.sorted_ids non-null: the padding rows of the experts' runs are zeroed.
+struct ScatterRows {
+    moe_dtype dtype;
+    const void* src;       // [M][H]
+    const float* weights;  // [M][topk]
+    const int32_t* pair_row;
+    int64_t nrows;  // rows of rows_in and rows_out
+    const void* rows_in;
+    void* rows_out;
+    float* dots;
+    moe_align_bufs al;
+    int M, topk, E, block_m, H;
+};
+hipError_t launch_scatter_rows(const ScatterRows& c, hipStream_t s);
+
+// The same from an alignment (no pair_row yet), which the call writes.
+hipError_t launch_permute(const ScatterRows& c, const int32_t* ids, int32_t* pair_row, hipStream_t s);
+
+// out[t] = sum_j w_tj rows[row of (t, j)]; with x: dots[p] = <rows[row of p], x[p / topk]>.
+struct GatherRows {
+    moe_dtype dtype, out_dtype;
+    const void* rows;
+    int64_t nrows;
+    const int32_t* pair_row;
+    const float* weights;
+    const void* x;
+    int M, topk, H;
+    void* out;
+    float* dots;
+};
+hipError_t launch_gather_rows(const GatherRows& c, hipStream_t s);
+
+// One row pass around a block (moe_residual_norm).
+struct NormCall {
+    moe_dtype dtype;
+    const void *h, *y;
+    moe_norm_spec n;
+    int M, H;
+    void *h_out, *x;
+};
+hipError_t launch_residual_norm(const NormCall& c, hipStream_t s);
+
+constexpr int kMaxNormH = 16384;  // a row is held in the registers of one workgroup
+
+struct NormGrad {
+    moe_dtype dtype;
+    const void *h_out, *dh_out, *dx, *y;
+    moe_norm_spec n;
+    int M, H;
+    void *dh, *dy;
+    float *dpost, *dgate, *dpre;
+    float* part;  // [norm_grad_groups(M, H)][3][H]
+};
+int norm_grad_groups(int M, int H);
+hipError_t launch_residual_norm_backward(const NormGrad& c, hipStream_t s);
+
+// Gradients of the grouped products (bfloat16 operands).
+struct GradCall {
+    const void* dc;  // [P][N] pair order
+    const void* a;   // dw: [M][K] (per token) or [P][K]
+    const void* w;   // dx: [E][N][K]
+    const void* z;   // dx through SiLU-and-mul: [P][2K]
+    moe_align_bufs al;
+    int M, topk, E, N, K, block_m;
+    bool per_token;
+    moe_dtype out_dtype;  // dw
+    void* out;            // dx: [P][K], or [P][2K] with z; dw: [E][N][K]
+    void* act;            // dx with z: [P][K] or NULL
+};
+hipError_t launch_grad_dx(const GradCall& c, hipStream_t s);
+hipError_t launch_grad_dw(const GradCall& c, hipStream_t s);
+
+// n bytes of zeros (a multiple of 16).
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,143 @@
+"""One residual block of a fine-grained layer forward and backward on the framework's
+calls, as a training step runs them, against float64 with the same roundings."""
+import pytest
+import torch
+
+import train_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_layer_topk_amd as moe
+    moe.lib()
+    return torch.device("cuda:0")
+
+
+def make(M, E, k, H, I, seed):
+    g = torch.Generator().manual_seed(seed)
+
+    def r(*shape, size=1.0, to=BF):
+        return (torch.randn(*shape, generator=g) * size).to(to)
+
+    return dict(h=r(M, H, size=2.0), w_in=(1 + r(H, size=0.1, to=torch.float32)).to(BF),
+                w_post=(1 + r(H, size=0.1, to=torch.float32)).to(BF), gate=r(H, size=0.5),
+                wr=r(E, H, size=0.05, to=torch.float32), w1=r(E, 2 * I, H, size=0.05), w2=r(E, H, I, size=0.05),
+                dout=r(M, H))
+
+
+def block(moe, p, M, E, k, H, I, scale, sorted_rows):
+    """Forward and backward; sorted_rows: through rows in expert order."""
+    _, x = moe.moe_residual_norm(p["h"], pre_weight=p["w_in"], eps=EPS)
+    logits = moe.moe_router_logits(x, p["wr"])
+    ids, wts = moe.moe_route(logits, k)
+    al = moe.moe_align(ids, E, 64)
+    z, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP, x, p["w1"], al, M, k)
+    act, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP_SILU, x, p["w1"], al, M, k)
+    y, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_DOWN, act, p["w2"], al, M, k)
+    if sorted_rows:  # the same rows by way of expert order (as another device would hold them)
+        one = ids.view(-1, 1)
+        al1 = moe.moe_align(one, E, 16)
+        rows, at = moe.moe_permute(y, one, al1)
+        at = at.view(M, k)
+        out = moe.moe_unpermute(rows, at, wts)
+    else:
+        out = moe.moe_combine(y, wts, k)
+    h_out, _ = moe.moe_residual_norm(p["h"], out, post_weight=p["w_post"], gate=p["gate"], scale=scale, eps=EPS)
+    # ---- backward
+    dh, dout, dpost, dgate, _ = moe.moe_residual_norm_backward(h_out, p["dout"], None, out, post_weight=p["w_post"],
+                                                               gate=p["gate"], scale=scale, eps=EPS)
+    if sorted_rows:
+        drows, dw = moe.moe_unpermute_backward(dout, rows, wts, at, drows=torch.zeros_like(rows))
+        dy, _ = moe.moe_permute_backward(drows, at.view(-1, 1))
+    else:
+        dy, dw = moe.moe_unpermute_backward(dout, y, wts)
+    dz, act_b = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_DOWN, dy, p["w2"], al, M, k, z=z)
+    dw2 = moe.moe_grouped_gemm_dw(moe.MOE_GEMM_DOWN, dy, act_b, al, M, k)
+    dxp, _ = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_GATE_UP, dz, p["w1"], al, M, k)
+    dw1 = moe.moe_grouped_gemm_dw(moe.MOE_GEMM_GATE_UP, dz, x, al, M, k)
+    dx, _ = moe.moe_permute_backward(dxp, topk=k)
+    dh_in, _, _, _, dw_in = moe.moe_residual_norm_backward(p["h"], dh, dx, pre_weight=p["w_in"], eps=EPS)
+    return dict(ids=ids, wts=wts, x=x, z=z, act=act_b, y=y, out=out, h_out=h_out, dh=dh, dout=dout, dpost=dpost,
+                dgate=dgate, dy=dy, dw=dw, dz=dz, dw1=dw1, dw2=dw2, dxp=dxp, dx=dx, dh_in=dh_in, dw_in=dw_in)
+
+
+def reference(p, got, M, E, k, H, I, scale):
+    """Every tensor in float64 from the call's own inputs as the run had them."""
+    q = {n: t.double().cpu() for n, t in p.items()}
+    v = {n: t.double().cpu() if t.is_floating_point() else t.cpu() for n, t in got.items()}
+    flat = v["ids"].reshape(-1)
+    want = dict(x=ref.rms_norm(q["h"], EPS) * q["w_in"])
+    lists = [(flat == e).nonzero().flatten() for e in range(E)]
+    for n, cols in (("z", 2 * I), ("act", I), ("y", H), ("dz", 2 * I), ("dxp", H)):
+        want[n] = torch.zeros(M * k, cols, dtype=torch.float64)
+    want["dw1"], want["dw2"] = torch.zeros_like(q["w1"]), torch.zeros_like(q["w2"])
+    for e, i in enumerate(lists):
+        want["z"][i] = v["x"][i // k] @ q["w1"][e].t()
+        want["act"][i] = ref.silu_mul(v["z"][i])
+        d = v["dy"][i] @ q["w2"][e]
+        gt, up = v["z"][i][:, :I], v["z"][i][:, I:]
+        s = torch.sigmoid(gt)
+        want["dz"][i] = torch.cat([d * up * s * (1 + gt * (1 - s)), d * gt * s], 1)
+        want["dxp"][i] = v["dz"][i] @ q["w1"][e]
+        want["dw1"][e] = v["dz"][i].t() @ v["x"][i // k]
+        want["dw2"][e] = v["dy"][i].t() @ v["act"][i]
+        want["y"][i] = v["act"][i] @ q["w2"][e].t()
+    yk = v["y"].view(M, k, H)
+    want["out"] = (yk * v["wts"][:, :, None]).sum(1)
+    want["h_out"], _ = ref.residual_norm(q["h"], v["out"], q["w_post"], q["gate"], scale, None, EPS)
+    out = v["out"].clone().requires_grad_()
+    post, gate = q["w_post"].clone().requires_grad_(), q["gate"].clone().requires_grad_()
+    step, _ = ref.residual_norm(torch.zeros_like(out), out, post, gate, scale, None, EPS)
+    want["dout"], want["dpost"], want["dgate"] = torch.autograd.grad(step, (out, post, gate), q["dout"])
+    want["dh"] = q["dout"]
+    want["dy"] = (v["dout"][:, None, :] * v["wts"][:, :, None]).reshape(M * k, H)
+    want["dw"] = (yk * v["dout"][:, None, :]).sum(2)
+    want["dx"] = v["dxp"].view(M, k, H).sum(1)
+    h, w_in = q["h"].clone().requires_grad_(), q["w_in"].clone().requires_grad_()
+    more, want["dw_in"] = torch.autograd.grad(ref.rms_norm(h, EPS) * w_in, (h, w_in), v["dx"])
+    want["dh_in"] = v["dh"] + more
+    return want, v
+
+
+@pytest.mark.parametrize("sorted_rows", [False, True])
+@pytest.mark.parametrize("M,E,k,H,I", [(1, 8, 2, 256, 128), (75, 16, 4, 384, 256), (260, 4, 2, 512, 384)])
+def test_block(dev, M, E, k, H, I, sorted_rows):
+    """Each result from the inputs that the run itself had: off by one rounding of the
+    result (2^-8 of its norm for bfloat16 rows; sums in float32 1e-5, which is over 400 U
+    times the ratio of a sum's magnitudes to its size here).  y comes from the fused
+    kind's act, whose z was not rounded: two roundings of z more, silu's slope at most 1.1."""
+    import moe_layer_topk_amd as moe
+    p = {n: t.to(dev) for n, t in make(M, E, k, H, I, 1).items()}
+    got = block(moe, p, M, E, k, H, I, 0.8, sorted_rows)
+    want, v = reference(p, got, M, E, k, H, I, 0.8)
+    for n, w in want.items():
+        rel = float((v[n] - w).norm() / w.norm())
+        f32 = n in ("dpost", "dgate", "dw", "dw_in")
+        bound = 1e-5 if f32 else 2.0 ** -8 * (4.5 if n == "y" else 1.0)
+        assert rel <= bound, f"{n}: {rel} of {bound}"
+
+
+def test_block_in_a_graph(dev):
+    """The whole step captured: replays on new inputs give the eager step's bits."""
+    import moe_layer_topk_amd as moe
+    M, E, k, H, I = 130, 8, 2, 256, 256
+    p = {n: t.to(dev) for n, t in make(M, E, k, H, I, 2).items()}
+    block(moe, p, M, E, k, H, I, 0.8, False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = block(moe, p, M, E, k, H, I, 0.8, False)
+    for i in range(4):
+        p["h"].copy_(make(M, E, k, H, I, 3 + i)["h"].to(dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in held.items()}
+        eager = block(moe, p, M, E, k, H, I, 0.8, False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[n], eager[n]) for n in got)
