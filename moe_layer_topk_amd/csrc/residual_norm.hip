@@ -8,21 +8,27 @@
 // and what is in place stays right: all of a row is read before any of it is
 // written.  h' goes to the second norm in float32, before its own rounding.
 // Bound by memory (16 bytes a lane and tensor).
+#include <algorithm>
+
 #include "moe_block.h"
 #include "moe_launch.h"
 #include "moe_train.h"
 
 namespace moe {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+// Rows are stored with the non-temporal hint: 16384 x 4096 bfloat16 rows 111 -> 94
+// us, the gradient at 4096 rows 47.8 -> 46.4 (the same hint on the loads: 107, 50).
 template <int DT>
 __device__ __forceinline__ void store8(void* x, size_t i, const float (&v)[8]) {
     if constexpr (DT == MOE_F32) {
-        float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(x) + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        u32x4* p = reinterpret_cast<u32x4*>(reinterpret_cast<float*>(x) + i);
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, make_float4(v[0], v[1], v[2], v[3])), p);
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, make_float4(v[4], v[5], v[6], v[7])), p + 1);
     } else {
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(x) + i) =
-            uint4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])};
+        __builtin_nontemporal_store(u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])},
+                                    reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(x) + i));
     }
 }
 
@@ -37,24 +43,23 @@ __device__ __forceinline__ float load1w(const void* w, bool bf, size_t i) {
     return bf ? bf2f(static_cast<const uint16_t*>(w)[i]) : static_cast<const float*>(w)[i];
 }
 
-// Sums of N values over the workgroup of T threads, in every thread.  `slot`
-// alternates between calls, so that one barrier a call is enough.
+// Sums of N values over the workgroup of T threads, in every thread, in a fixed
+// order.  A caller alternates between two `lds`, so that one barrier a call is
+// enough.
 template <int T, int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float (*lds)[N]) {
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*lds)[T / 64]) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) v[n] += __shfl_xor(v[n], off, 64);
+    for (int n = 0; n < N; ++n) v[n] = wave_sum_f32(v[n]);
     if constexpr (T > 64) {
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
-            for (int n = 0; n < N; ++n) lds[threadIdx.x >> 6][n] = v[n];
+            for (int n = 0; n < N; ++n) lds[n][threadIdx.x >> 6] = v[n];
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < T / 64; ++w) s += lds[w][n];
+            for (int w = 0; w < T / 64; ++w) s += lds[n][w];
             v[n] = s;
         }
     }
@@ -63,7 +68,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*lds)[N]) {
 // T threads, 8 V columns a thread.
 template <int DT, int T, int V>
 __global__ void __launch_bounds__(T) residual_norm_kernel(NormCall c) {
-    __shared__ float lds[2][T / 64][1];
+    __shared__ __attribute__((aligned(16))) float lds[2][1][T / 64];
     const int t = blockIdx.x, tid = threadIdx.x;
     const size_t row = (size_t)t * c.H;
     const bool bf = c.n.w_dtype == MOE_BF16;
@@ -130,51 +135,135 @@ __global__ void __launch_bounds__(T) residual_norm_kernel(NormCall c) {
     }
 }
 
+// 16 bytes of a row as loaded: 8 bfloat16 or 4 float32 values.
+template <int DT>
+struct Raw {
+    static constexpr int E = DT == MOE_F32 ? 4 : 8;
+    uint4 q;
+    __device__ __forceinline__ void load(const void* x, size_t i) {
+        q = *reinterpret_cast<const uint4*>(static_cast<const char*>(x) + i * (16 / E));
+    }
+    __device__ __forceinline__ void zero() { q = uint4{0, 0, 0, 0}; }
+    __device__ __forceinline__ float at(int k) const {
+        const int n = DT == MOE_F32 ? k : k / 2;
+        const uint32_t w = n == 0 ? q.x : n == 1 ? q.y : n == 2 ? q.z : q.w;
+        if constexpr (DT == MOE_F32) return __uint_as_float(w);
+        return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
+    }
+    __device__ __forceinline__ static void store(void* x, size_t i, const float (&v)[E]) {
+        u32x4 o;
+        if constexpr (DT == MOE_F32)
+            o = __builtin_bit_cast(u32x4, make_float4(v[0], v[1], v[2], v[3]));
+        else
+            o = u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4 % E], v[5 % E]), pack_bf2(v[6 % E], v[7 % E])};
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<char*>(x) + i * (16 / E)));
+    }
+};
+
+// E (8 or 4) weights.
+template <int E>
+__device__ __forceinline__ void load_w(const void* w, bool bf, size_t i, float* v) {
+#pragma unroll
+    for (int k = 0; k < E; k += 4) {
+        if (bf) {
+            const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + i + k);
+            v[k] = __uint_as_float(a.x << 16), v[k + 1] = __uint_as_float(a.x & 0xffff0000u);
+            v[k + 2] = __uint_as_float(a.y << 16), v[k + 3] = __uint_as_float(a.y & 0xffff0000u);
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + i + k);
+            v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
+        }
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void store_part(float* x, const float (&v)[E]) {
+#pragma unroll
+    for (int k = 0; k < E; k += 4) *reinterpret_cast<float4*>(x + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+}
+
+// The rows a thread of the gradient kernel reads: its columns of h', dx, dh' and y.
+template <int DT, int T, int V>
+struct GradRow {
+    Raw<DT> h[V], dx[V], dh[V], y[V];
+    __device__ __forceinline__ void load(const NormGrad& c, int t, bool pre) {
+        const size_t row = (size_t)t * c.H;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = (i * T + (int)threadIdx.x) * Raw<DT>::E;
+            const bool in = col < c.H;
+            if (in && pre) h[i].load(c.h_out, row + col), dx[i].load(c.dx, row + col);
+            else h[i].zero(), dx[i].zero();
+            if (in && c.dh_out) dh[i].load(c.dh_out, row + col);
+            else dh[i].zero();
+            if (in && c.y) y[i].load(c.y, row + col);
+            else y[i].zero();
+        }
+    }
+};
+
 // Gradients.  With n = v r the normed row of v and q = d w the gradient at n,
 // the gradient of v is r (q - n mean(q n)), and w's is the sum over rows of d n.
 // A workgroup takes rows t, t + groups, ... and keeps its part of the three column
-// sums in registers; norm_parts_kernel adds the parts in order.
-template <int DT, int T, int V>
-__global__ void __launch_bounds__(T) residual_norm_backward_kernel(NormGrad c) {
-    __shared__ float lds1[2][T / 64][3];
-    __shared__ float lds2[2][T / 64][2];
+// sums in registers; norm_parts_kernel adds the parts in order.  kHold: the weights
+// stay in registers; kNext: the next row is on its way while this one waits for its
+// sums (a row may be written over one of its inputs, never over another row's).
+template <int DT, int T, int V, bool kHold, bool kNext, int W>
+__global__ void __launch_bounds__(T, W) residual_norm_backward_kernel(NormGrad c) {
+    __shared__ __attribute__((aligned(16))) float lds1[2][3][T / 64];
+    __shared__ __attribute__((aligned(16))) float lds2[2][2][T / 64];
+    constexpr int E = Raw<DT>::E;
     const int tid = threadIdx.x;
     const bool bf = c.n.w_dtype == MOE_BF16;
     const bool pre = c.n.pre_weight != nullptr, post = c.n.post_weight != nullptr;
     const bool gate_c = c.n.gate && !c.n.gate_per_token, gate_t = c.n.gate && c.n.gate_per_token;
     const float inv_h = 1.0f / (float)c.H;
-    float apost[V][8], agate[V][8], apre[V][8];
+    float wpre[kHold ? E * V : 1], wpost[kHold ? E * V : 1], wgate[kHold ? E * V : 1];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int k = 0; k < E * V; ++k) wpre[k] = wpost[k] = wgate[k] = 1.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = (i * T + tid) * E;
+            if (col >= c.H) continue;
+            if (pre) load_w<E>(c.n.pre_weight, bf, col, wpre + E * i);
+            if (post) load_w<E>(c.n.post_weight, bf, col, wpost + E * i);
+            if (gate_c) load_w<E>(c.n.gate, bf, col, wgate + E * i);
+        }
+    }
+    float apost[V][E], agate[V][E], apre[V][E];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) apost[i][k] = agate[i][k] = apre[i][k] = 0.0f;
+        for (int k = 0; k < E; ++k) apost[i][k] = agate[i][k] = apre[i][k] = 0.0f;
+    GradRow<DT, T, V> in, next;
+    if (kNext && (int)blockIdx.x < c.M) next.load(c, blockIdx.x, pre);
     int odd = 0;
     for (int t = blockIdx.x; t < c.M; t += gridDim.x, odd ^= 1) {
         const size_t row = (size_t)t * c.H;
-        float y[V][8], h[V][8], dx[V][8], dh[V][8];
+        if constexpr (kNext) {
+            in = next;
+            if (t + (int)gridDim.x < c.M) next.load(c, t + gridDim.x, pre);
+        } else {
+            in.load(c, t, pre);
+        }
+        float dh[V][E];
         float s[3] = {0.0f, 0.0f, 0.0f};  // y^2, h'^2, dx w_pre h'
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int col = (i * T + tid) * 8;
+            const int col = (i * T + tid) * E;
+            float w[E];
+            if constexpr (!kHold) {
+                if (pre && col < c.H) load_w<E>(c.n.pre_weight, bf, col, w);
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[i][k] = h[i][k] = dx[i][k] = dh[i][k] = 0.0f;
-            if (col >= c.H) continue;
-            if (pre) load8<DT>(c.h_out, row + col, h[i]);
-            if (pre) load8<DT>(c.dx, row + col, dx[i]);
-            if (c.dh_out) load8<DT>(c.dh_out, row + col, dh[i]);
-            if (c.y) load8<DT>(c.y, row + col, y[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int col = (i * T + tid) * 8;
-            float w[8];
-            if (pre && col < c.H) load8w(c.n.pre_weight, bf, col, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                s[0] = fmaf(y[i][k], y[i][k], s[0]);
+            for (int k = 0; k < E; ++k) {
+                const float y = in.y[i].at(k), h = in.h[i].at(k);
+                dh[i][k] = in.dh[i].at(k);
+                s[0] = fmaf(y, y, s[0]);
                 if (pre && col < c.H) {
-                    s[1] = fmaf(h[i][k], h[i][k], s[1]);
-                    s[2] = fmaf(dx[i][k] * w[k], h[i][k], s[2]);
+                    s[1] = fmaf(h, h, s[1]);
+                    s[2] = fmaf(in.dx[i].at(k) * (kHold ? wpre[kHold ? E * i + k : 0] : w[k]), h, s[2]);
                 }
             }
         }
@@ -185,22 +274,22 @@ __global__ void __launch_bounds__(T) residual_norm_backward_kernel(NormGrad c) {
             const float m = s[2] * r2 * inv_h;  // mean of q n
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int col = (i * T + tid) * 8;
+                const int col = (i * T + tid) * E;
                 if (col >= c.H) continue;
-                float w[8];
-                load8w(c.n.pre_weight, bf, col, w);
+                float w[E];
+                if constexpr (!kHold) load_w<E>(c.n.pre_weight, bf, col, w);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float n = h[i][k] * r2;
-                    apre[i][k] = fmaf(dx[i][k], n, apre[i][k]);
-                    dh[i][k] += r2 * (dx[i][k] * w[k] - n * m);
+                for (int k = 0; k < E; ++k) {
+                    const float n = in.h[i].at(k) * r2;
+                    apre[i][k] = fmaf(in.dx[i].at(k), n, apre[i][k]);
+                    dh[i][k] += r2 * (in.dx[i].at(k) * (kHold ? wpre[kHold ? E * i + k : 0] : w[k]) - n * m);
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int col = (i * T + tid) * 8;
-            if (col < c.H) store8<DT>(c.dh, row + col, dh[i]);
+            const int col = (i * T + tid) * E;
+            if (col < c.H) Raw<DT>::store(c.dh, row + col, dh[i]);
         }
         if (!c.y) continue;
         // du = s g dh'; through the post norm
@@ -208,20 +297,23 @@ __global__ void __launch_bounds__(T) residual_norm_backward_kernel(NormGrad c) {
         const float gt = gate_t ? load1w(c.n.gate, bf, t) : 1.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int col = (i * T + tid) * 8;
+            const int col = (i * T + tid) * E;
             if (col >= c.H) continue;
-            float w[8], g[8];
-            if (post) load8w(c.n.post_weight, bf, col, w);
-            if (gate_c) load8w(c.n.gate, bf, col, g);
+            float w[E], g[E];
+            if constexpr (!kHold) {
+                if (post) load_w<E>(c.n.post_weight, bf, col, w);
+                if (gate_c) load_w<E>(c.n.gate, bf, col, g);
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float n = y[i][k] * r1, u = post ? n * w[k] : n;
+            for (int k = 0; k < E; ++k) {
+                const float wp = kHold ? wpost[kHold ? E * i + k : 0] : post ? w[k] : 1.0f;
+                const float n = in.y[i].at(k) * r1, u = n * wp;
                 const float d = c.n.scale * dh[i][k];  // at g u
                 agate[i][k] = fmaf(d, u, agate[i][k]);
                 s2[1] = fmaf(d, u, s2[1]);
-                const float du = d * (gate_c ? g[k] : gt);
+                const float du = d * (gate_c ? (kHold ? wgate[kHold ? E * i + k : 0] : g[k]) : gt);
                 apost[i][k] = fmaf(du, n, apost[i][k]);
-                const float q = post ? du * w[k] : du;
+                const float q = du * wp;
                 s2[0] = fmaf(q, n, s2[0]);
                 dh[i][k] = q;
             }
@@ -231,34 +323,51 @@ __global__ void __launch_bounds__(T) residual_norm_backward_kernel(NormGrad c) {
         if (gate_t && tid == 0 && c.dgate) c.dgate[t] = s2[1];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int col = (i * T + tid) * 8;
+            const int col = (i * T + tid) * E;
             if (col >= c.H) continue;
-            float o[8];
+            float o[E];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = post ? r1 * (dh[i][k] - y[i][k] * r1 * m) : dh[i][k];
-            store8<DT>(c.dy, row + col, o);
+            for (int k = 0; k < E; ++k) o[k] = post ? r1 * (dh[i][k] - in.y[i].at(k) * r1 * m) : dh[i][k];
+            Raw<DT>::store(c.dy, row + col, o);
         }
     }
     float* part = c.part + (size_t)blockIdx.x * 3 * c.H;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int col = (i * T + tid) * 8;
+        const int col = (i * T + tid) * E;
         if (col >= c.H) continue;
-        if (c.dpost) store8<MOE_F32>(part, col, apost[i]);
-        if (c.dgate && gate_c) store8<MOE_F32>(part, (size_t)c.H + col, agate[i]);
-        if (c.dpre) store8<MOE_F32>(part, (size_t)2 * c.H + col, apre[i]);
+        if (c.dpost) store_part(part + col, apost[i]);
+        if (c.dgate && gate_c) store_part(part + c.H + col, agate[i]);
+        if (c.dpre) store_part(part + 2 * c.H + col, apre[i]);
     }
 }
 
-// Sums of the groups' parts: blockIdx.y the vector, a thread a column.
-__global__ void __launch_bounds__(64) norm_parts_kernel(const float* __restrict__ part, int groups, int H, float* dpost,
-                                                        float* dgate, float* dpre) {
+// Sums of the groups' parts: blockIdx.y the vector; 16 lanes take 64 columns, 64
+// slices of the groups meet in LDS, all in a fixed order.
+__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* __restrict__ part, int groups, int H, float* dpost,
+                                                         float* dgate, float* dpre) {
+    __shared__ float lds[64][64];
     float* out = blockIdx.y == 0 ? dpost : blockIdx.y == 1 ? dgate : dpre;
-    const int col = blockIdx.x * 64 + threadIdx.x;
-    if (!out || col >= H) return;
-    float s = 0.0f;
-    for (int g = 0; g < groups; ++g) s += part[((size_t)g * 3 + blockIdx.y) * H + col];
-    out[col] = s;
+    if (!out) return;
+    const int slice = threadIdx.x >> 4, c4 = (threadIdx.x & 15) * 4, col = blockIdx.x * 64 + c4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < H) {
+        const float* p = part + (size_t)blockIdx.y * H + col;
+#pragma unroll 8
+        for (int g = slice; g < groups; g += 64) {
+            const float4 v = *reinterpret_cast<const float4*>(p + (size_t)g * 3 * H);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+    }
+    *reinterpret_cast<float4*>(&lds[slice][c4]) = s;
+    __syncthreads();
+    const int o = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && o < H) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) t += lds[i][threadIdx.x];
+        out[o] = t;
+    }
 }
 
 template <int DT, int T, int V>
@@ -269,10 +378,15 @@ static hipError_t norm_tv(const NormCall& c, hipStream_t s) {
 
 template <int DT>
 static hipError_t norm_dt(const NormCall& c, hipStream_t s) {
-    if (c.H <= 512) return norm_tv<DT, 64, 1>(c, s);
-    if (c.H <= 2048) return norm_tv<DT, 256, 1>(c, s);
-    if (c.H <= 4096) return norm_tv<DT, 512, 1>(c, s);
-    if (c.H <= 8192) return norm_tv<DT, 1024, 1>(c, s);
+    // Two pieces a thread for bfloat16, one for float32 (64 Mi elements, h and y in,
+    // h_out and x out, H = 4096: bfloat16 76 us, one piece 99, four 80; float32 one 195
+    // at H = 2048, two 207)
+    constexpr int V = DT == MOE_BF16 ? 2 : 1;
+    if (c.H <= 512 * V) return norm_tv<DT, 64, V>(c, s);
+    if (c.H <= 1024 * V) return norm_tv<DT, 128, V>(c, s);
+    if (c.H <= 2048 * V) return norm_tv<DT, 256, V>(c, s);
+    if (c.H <= 4096 * V) return norm_tv<DT, 512, V>(c, s);
+    if (c.H <= 8192 * V) return norm_tv<DT, 1024, V>(c, s);
     return norm_tv<DT, 1024, 2>(c, s);
 }
 
@@ -280,21 +394,37 @@ hipError_t launch_residual_norm(const NormCall& c, hipStream_t s) {
     return c.dtype == MOE_BF16 ? norm_dt<MOE_BF16>(c, s) : norm_dt<MOE_F32>(c, s);
 }
 
-int norm_grad_groups(int M, int H) { return M < 512 ? M : 512; }
+// Workgroups of the gradient kernel: two of 512 threads a CU, as many threads of
+// smaller ones (at 4096 x 4096 512 45 us, 256 49, 768 53), but eight rows each where
+// there are rows enough, since every group leaves 12 bytes a column to be added.
+int norm_grad_groups(int M, int H) {
+    const int most = H > 2048 ? 512 : 1024;
+    const int g = M / 8 < 256 ? 256 : M / 8;
+    return std::min(M, std::min(g, most));
+}
 
-template <int DT, int T, int V>
+template <int DT, int T, int V, int W, bool kHold>
 static hipError_t grad_tv(const NormGrad& c, int groups, hipStream_t s) {
-    hipLaunchKernelGGL((residual_norm_backward_kernel<DT, T, V>), dim3(groups), dim3(T), 0, s, c);
+    hipLaunchKernelGGL((residual_norm_backward_kernel<DT, T, V, kHold, kHold, W>), dim3(groups), dim3(T), 0, s, c);
     return hipGetLastError();
 }
 
+// One 16-byte piece a thread, the weights and the next row in registers (4096 x
+// 4096 bfloat16 45 us; without the next row 47, without either 49; two pieces a
+// thread 47-97), until a workgroup has no more threads.
 template <int DT>
 static hipError_t grad_dt(const NormGrad& c, int groups, hipStream_t s) {
-    if (c.H <= 512) return grad_tv<DT, 64, 1>(c, groups, s);
-    if (c.H <= 2048) return grad_tv<DT, 256, 1>(c, groups, s);
-    if (c.H <= 4096) return grad_tv<DT, 512, 1>(c, groups, s);
-    if (c.H <= 8192) return grad_tv<DT, 1024, 1>(c, groups, s);
-    return grad_tv<DT, 1024, 2>(c, groups, s);
+    constexpr int E = Raw<DT>::E;
+    if (c.H <= 64 * E) return grad_tv<DT, 64, 1, 4, true>(c, groups, s);
+    if (c.H <= 128 * E) return grad_tv<DT, 128, 1, 4, true>(c, groups, s);
+    if (c.H <= 256 * E) return grad_tv<DT, 256, 1, 4, true>(c, groups, s);
+    if (c.H <= 512 * E) return grad_tv<DT, 512, 1, 4, true>(c, groups, s);
+    if (c.H <= 1024 * E) return grad_tv<DT, 1024, 1, 4, true>(c, groups, s);
+    // longer rows: pieces in a line, half as many wavefronts with all of the
+    // registers (16384 columns, 1024 rows: bfloat16 102 us, on 1024 threads 147 with
+    // registers spilled; float32 188 and 210)
+    if (DT == MOE_F32 && c.H <= 2048 * E) return grad_tv<DT, 512, 4, 2, false>(c, groups, s);
+    return grad_tv<DT, 512, DT == MOE_F32 ? 8 : 4, 2, false>(c, groups, s);
 }
 
 hipError_t launch_residual_norm_backward(const NormGrad& c, hipStream_t s) {
@@ -303,7 +433,7 @@ hipError_t launch_residual_norm_backward(const NormGrad& c, hipStream_t s) {
     if (e != hipSuccess) return e;
     float* dgate = c.n.gate_per_token ? nullptr : c.dgate;
     if (!c.dpost && !dgate && !c.dpre) return hipSuccess;
-    hipLaunchKernelGGL(norm_parts_kernel, dim3((c.H + 63) / 64, 3), dim3(64), 0, s, c.part, groups, c.H, c.dpost, dgate,
+    hipLaunchKernelGGL(norm_parts_kernel, dim3((c.H + 63) / 64, 3), dim3(1024), 0, s, c.part, groups, c.H, c.dpost, dgate,
                        c.dpre);
     return hipGetLastError();
 }
