@@ -287,8 +287,8 @@ hipError_t launch_grad_dx(const GradCall& c, hipStream_t s) {
 struct DwCfg {
     static constexpr int ST = 4, Threads = 512, RP = 32;
     static constexpr int HalfBytes = RP * 512, StageBytes = 2 * HalfBytes;
-    static constexpr int Ids = 4096;  // rows between refills of the id list
-    static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + Ids * 4;
+    static constexpr int Ids = 2048;  // rows between refills of the row lists
+    static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + Ids * 8;
     static constexpr int L = 4;  // copies a wave and stage: two of dc's rows, two of a's
 };
 
@@ -310,17 +310,21 @@ grad_dw_kernel(GradCall g, int n_tiles, int k_tiles, int per_xcd) {
     const int wn = wave >> 1, wk = wave & 1;
     const int count = g.al.expert_counts[e];
     const int32_t* sorted = g.al.sorted_ids + g.al.expert_offsets[e];
-    int* ids_s = reinterpret_cast<int*>(grad_lds + C::IdsOffset);
+    int2* ids_s = reinterpret_cast<int2*>(grad_lds + C::IdsOffset);  // rows of dc and of a, -1: zeros
 
-    // copy j of the wave: rows 4 wave + 2 j and the next of a stage, 32 lanes each
-    const char* zeros = reinterpret_cast<const char*>(grad_zeros);
+    // copy j of the wave: rows 4 wave + 2 j and the next of a stage, 32 lanes each.
+    // A lane whose columns lie past the matrix reads zeros.
+    const char* zeros = reinterpret_cast<const char*>(grad_zeros) + (lane & 31) * 16;
     const int c = lane & 31, lrow = 4 * wave + (lane >> 5);
-    int ncol[2], kcol[2];  // the lane's first column of dc and of a (copy j)
+    const char *abase[2], *bbase[2];
+    unsigned ald[2], bld[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int lc = (tr_place(c >> 1, lrow + 2 * j) * 2 + (c & 1)) * 8;
-        ncol[j] = n0 + lc;
-        kcol[j] = k0 + lc;
+        abase[j] = n0 + lc < N ? static_cast<const char*>(g.dc) + (size_t)(n0 + lc) * 2 : zeros;
+        bbase[j] = k0 + lc < K ? static_cast<const char*>(g.a) + (size_t)(k0 + lc) * 2 : zeros;
+        ald[j] = n0 + lc < N ? (unsigned)N * 2 : 0;
+        bld[j] = k0 + lc < K ? (unsigned)K * 2 : 0;
     }
     const unsigned lds0 = lds_addr_of(grad_lds);
     f32x16 acc[2][4];
@@ -337,53 +341,70 @@ grad_dw_kernel(GradCall g, int n_tiles, int k_tiles, int per_xcd) {
     for (int j = 0; j < 4; ++j) klane[j] = C::HalfBytes + tr_lane(lane, wk * 128 + 32 * j);
 
     for (int base = 0; base < count; base += C::Ids) {
-        const int n = min(C::Ids, count - base);
+        const int n = min(C::Ids, count - base), nst = (n + C::RP - 1) / C::RP;
         __syncthreads();
-        for (int i = tid; i < n; i += C::Threads) ids_s[i] = sorted[base + i];
-        __syncthreads();
-        const int nst = (n + C::RP - 1) / C::RP;
-        auto issue = [&](int kt) {
-            const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = kt * C::RP + lrow + 2 * j;
-                const char *pa = zeros + (lane & 31) * 16, *pb = pa;
-                if (r < n) {
-                    const int p = ids_s[r];
-                    if (ncol[j] < N) pa = static_cast<const char*>(g.dc) + ((size_t)p * N + ncol[j]) * 2;
-                    const int q = g.per_token ? p / g.topk : p;
-                    if (kcol[j] < K) pb = static_cast<const char*>(g.a) + ((size_t)q * K + kcol[j]) * 2;
-                }
-                const unsigned at = st + (4 * wave + 2 * j) * 512;
-                lds_dma16_at(pa, at);
-                lds_dma16_at(pb, at + C::HalfBytes);
-            }
-        };
-#pragma unroll
-        for (int s0 = 0; s0 < C::ST - 1; ++s0)
-            if (s0 < nst) issue(s0);
-        for (int kt = 0; kt < nst; ++kt) {
-            const int later = min(C::ST - 2, nst - 1 - kt);  // stages in flight behind this one
-            if (later == 2) wait_vm<2 * C::L>();
-            else if (later == 1) wait_vm<C::L>();
-            else wait_vm<0>();
-            __syncthreads();
-            if (kt + C::ST - 1 < nst) issue(kt + C::ST - 1);
-            const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 nf[2], kf[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) nf[i] = tr_read8(st + nlane[i] + ks * 16 * 512);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) kf[j] = tr_read8(st + klane[j] + ks * 16 * 512);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[j], nf[i], acc[i][j], 0, 0, 0);
-            }
+        for (int i = tid; i < nst * C::RP; i += C::Threads) {
+            const int p = i < n ? sorted[base + i] : -1;
+            ids_s[i] = int2{p, g.per_token && p >= 0 ? p / g.topk : p};
         }
+        __syncthreads();
+        int2 id[2];  // of the next stage to be copied
+        auto fetch_ids = [&](int kt) {
+            id[0] = ids_s[kt * C::RP + lrow];
+            id[1] = ids_s[kt * C::RP + lrow + 2];
+        };
+        auto issue = [&](int kt, int j) {
+            const char* pa = abase[j] + (size_t)(unsigned)id[j].x * ald[j];
+            const char* pb = bbase[j] + (size_t)(unsigned)id[j].y * bld[j];
+            pa = id[j].x < 0 ? zeros : pa;
+            pb = id[j].x < 0 ? zeros : pb;
+            const unsigned at = lds0 + (unsigned)((kt % C::ST) * C::StageBytes) + (4 * wave + 2 * j) * 512;
+            lds_dma16_at(pa, at);
+            lds_dma16_at(pb, at + C::HalfBytes);
+        };
+        for (int s0 = 0; s0 < C::ST - 1; ++s0)
+            if (s0 < nst) {
+                fetch_ids(s0);
+                issue(s0, 0);
+                issue(s0, 1);
+            }
+        if (C::ST - 1 < nst) fetch_ids(C::ST - 1);
+        auto stage = [&](int kt, auto pf_tag) {
+            constexpr bool pf = decltype(pf_tag)::value;
+            if constexpr (pf)
+                wait_vm<(C::ST - 2) * C::L>();
+            else
+                wait_vm_runtime<C::L>(min(C::ST - 2, nst - 1 - kt));
+            __syncthreads();
+            const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+            bf16x8 nf[2][2], kf[2][4];
+            auto read = [&](int ks) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) nf[ks][i] = tr_read8(st + nlane[i] + ks * 16 * 512);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kf[ks][j] = tr_read8(st + klane[j] + ks * 16 * 512);
+            };
+            read(0);
+            __builtin_amdgcn_sched_barrier(0);
+            read(1);
+            if (pf) issue(kt + C::ST - 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc[q / 4][q % 4] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[0][q % 4], nf[0][q / 4], acc[q / 4][q % 4], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (pf) {
+                issue(kt + C::ST - 1, 1);
+                if (kt + C::ST < nst) fetch_ids(kt + C::ST);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc[q / 4][q % 4] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[1][q % 4], nf[1][q / 4], acc[q / 4][q % 4], 0, 0, 0);
+        };
+        const int nmain = max(0, nst - (C::ST - 1));
+        for (int kt = 0; kt < nmain; ++kt) stage(kt, std::true_type{});
+        for (int kt = nmain; kt < nst; ++kt) stage(kt, std::false_type{});
     }
 
     // ---- epilogue: 32 n rows of the wave's tile at a time through LDS
