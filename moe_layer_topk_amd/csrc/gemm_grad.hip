@@ -21,6 +21,7 @@
 namespace moe {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kXcds = 8;
@@ -61,17 +62,17 @@ __device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
 
 template <int BM>
 struct DxCfg {
-    static constexpr int ST = 3, Threads = 256;
-    static constexpr int ABytes = BM * 128, WBytes = 64 * 512, StageBytes = ABytes + WBytes;
-    static constexpr int ALoads = BM / 8 / 4, WLoads = 8, L = ALoads + WLoads;  // copies a wave and stage
+    static constexpr int ST = 3, Threads = 256, NS = 32;  // NS: terms n a stage
+    static constexpr int ABytes = BM * NS * 2, WBytes = NS * 512, StageBytes = ABytes + WBytes;
+    static constexpr int ALoads = BM / 16 / 4, WLoads = NS / 8, L = ALoads + WLoads;  // copies a wave and stage
     static constexpr int TM = BM / 64, TN = 4;
     static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + BM * 4;
-    // chunk c of 16 bytes of row r (rows of 128 bytes)
-    __device__ static __forceinline__ int swz(int c, int r) { return c ^ ((r >> 1) & 7); }
+    // chunk c of 16 bytes of row r (rows of 64 bytes)
+    __device__ static __forceinline__ int swz(int c, int r) { return c ^ ((r >> 2) & 3); }
 };
 
-template <int BM, bool SILU>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2)))
+template <int BM, bool SILU, bool NTW>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
     using C = DxCfg<BM>;
     extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
@@ -100,10 +101,10 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
     const char* asrc[C::ALoads];
 #pragma unroll
     for (int j = 0; j < C::ALoads; ++j) {
-        const int r = (wave * C::ALoads + j) * 8 + (lane >> 3);
+        const int r = (wave * C::ALoads + j) * 16 + (lane >> 2);
         int p = sorted[r];
         if ((unsigned)p >= (unsigned)P) p = sorted[0];  // padding: any row, its results are dropped
-        asrc[j] = static_cast<const char*>(g.dc) + (size_t)p * N * 2 + C::swz(lane & 7, r) * 16;
+        asrc[j] = static_cast<const char*>(g.dc) + (size_t)p * N * 2 + C::swz(lane & 3, r) * 16;
     }
     // (columns past K read the next row, past the last row zeros; they are dropped)
     const v4i_rsrc wrsrc = buf_rsrc(static_cast<const char*>(g.w) + (size_t)e * N * K * 2, (unsigned)((size_t)N * K * 2));
@@ -120,9 +121,12 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
         for (int j = 0; j < C::L; ++j) {
             if (j < j0 || j >= j1) continue;
             if (j < C::ALoads)
-                lds_dma16_at(asrc[j] + (size_t)kt * 128, st + (wave * C::ALoads + j) * 1024);
+                lds_dma16_at(asrc[j] + (size_t)kt * (C::NS * 2), st + (wave * C::ALoads + j) * 1024);
+            else if constexpr (NTW)
+                lds_dma16_buf_nt(wrsrc, wsrc[j - C::ALoads], (unsigned)((size_t)kt * (C::NS * 2) * K),
+                                 st + C::ABytes + (wave * C::WLoads + (j - C::ALoads)) * 1024);
             else
-                lds_dma16_buf(wrsrc, wsrc[j - C::ALoads], (unsigned)((size_t)kt * 128 * K),
+                lds_dma16_buf(wrsrc, wsrc[j - C::ALoads], (unsigned)((size_t)kt * (C::NS * 2) * K),
                               st + C::ABytes + (wave * C::WLoads + (j - C::ALoads)) * 1024);
         }
     };
@@ -144,7 +148,7 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
     const int nreal = min(BM, g.al.expert_offsets[e] + g.al.expert_counts[e] - mtile * BM);
     const int live = __builtin_amdgcn_readfirstlane(min(C::TM, max(0, (nreal - wm * (BM / 2) + 31) / 32)));
 
-    const int nk = N / 64;
+    const int nk = N / C::NS;
 #pragma unroll
     for (int s0 = 0; s0 < C::ST - 1; ++s0)
         if (s0 < nk) issue_part(s0, 0, C::L);
@@ -163,18 +167,18 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
             const int c = ks * 2 + (lane >> 5);
 #pragma unroll
             for (int i = 0; i < LT; ++i)
-                af[buf][i] = *reinterpret_cast<const bf16x8*>(sa + arow[i] * 128 + (C::swz(c, arow[i]) << 4));
+                af[buf][i] = *reinterpret_cast<const bf16x8*>(sa + arow[i] * (C::NS * 2) + (C::swz(c, arow[i]) << 4));
 #pragma unroll
             for (int j = 0; j < C::TN; ++j)
                 if (LT) wf[buf][j] = tr_read8(st + wlane[j] + ks * 16 * 512);
         };
         read_frags(0, 0);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
+        for (int ks = 0; ks < C::NS / 16; ++ks) {
             const int cur = ks & 1;
-            if (ks < 3) read_frags(cur ^ 1, ks + 1);
+            if (ks + 1 < C::NS / 16) read_frags(cur ^ 1, ks + 1);
             // this substep's share of the next copies, between the products
-            const int j0 = ks * C::L / 4, j1 = (ks + 1) * C::L / 4;
+            const int j0 = ks * C::L / (C::NS / 16), j1 = (ks + 1) * C::L / (C::NS / 16);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int q = 0; q < C::TM * C::TN; ++q) {
@@ -202,78 +206,100 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
     else
         kloop(std::integral_constant<int, 0>{});
 
-    // ---- epilogue: the wave's tile through LDS (rows of 128 columns, 16 bytes of
-    // padding), so that memory sees whole lines
+    // ---- epilogue: 32 rows x 64 columns at a time through the wave's LDS (rows padded by
+    // 16 bytes), so that memory sees whole lines
     __syncthreads();
-    constexpr int kElem = SILU ? 4 : 2, kRow = 128 * kElem + 16, kRows = BM / 2;
-    static_assert(4 * kRows * kRow <= C::IdsOffset, "epilogue");
-    char* mine = grad_lds + wave * kRows * kRow;
+    constexpr int kElem = SILU ? 4 : 2, kRow = 64 * kElem + 16;
+    static_assert(4 * 32 * kRow <= C::IdsOffset, "epilogue");
+    char* mine = grad_lds + wave * 32 * kRow;
+    const int c8 = (lane & 7) * 8;
 #pragma unroll
-    for (int i = 0; i < C::TM; ++i)
+    for (int i = 0; i < C::TM; ++i) {
+        if (i >= live) break;
+        const int r0 = wm * (BM / 2) + 32 * i, rows = min(32, nreal - r0);
 #pragma unroll
-        for (int j = 0; j < C::TN; ++j)
+        for (int jh = 0; jh < 2; ++jh) {
+            const int col = k0 + wn * 128 + 64 * jh + c8;
+            size_t p[4];
+            uint4 zg[4], zu[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                char* at = mine + (32 * i + (lane & 31)) * kRow + (32 * j + 8 * v + 4 * (lane >> 5)) * kElem;
-                const float x0 = acc[i][j][4 * v], x1 = acc[i][j][4 * v + 1], x2 = acc[i][j][4 * v + 2],
-                            x3 = acc[i][j][4 * v + 3];
-                if constexpr (SILU)
-                    *reinterpret_cast<float4*>(at) = make_float4(x0, x1, x2, x3);
-                else
-                    *reinterpret_cast<uint2*>(at) = uint2{pack_bf2(x0, x1), pack_bf2(x2, x3)};
+            for (int q = 0; q < 4; ++q) {
+                const int r = 8 * q + (lane >> 3);
+                p[q] = (size_t)ids_s[r0 + min(r, rows - 1)];
+                if (SILU && col < K) {
+                    const uint16_t* z = static_cast<const uint16_t*>(g.z) + p[q] * 2 * K + col;
+                    zg[q] = *reinterpret_cast<const uint4*>(z), zu[q] = *reinterpret_cast<const uint4*>(z + K);
+                }
             }
-    const int c8 = (lane & 15) * 8, col = k0 + wn * 128 + c8;
-    if (col >= K) return;
-    const int rows = min(kRows, nreal - wm * kRows);
-    for (int r = lane >> 4; r < rows; r += 4) {
-        const size_t p = (size_t)ids_s[wm * kRows + r];
-        const char* at = mine + r * kRow + c8 * kElem;
-        if constexpr (SILU) {
-            const uint16_t* z = static_cast<const uint16_t*>(g.z) + p * 2 * K + col;
-            const uint4 zg = *reinterpret_cast<const uint4*>(z), zu = *reinterpret_cast<const uint4*>(z + K);
-            const float4 d0 = *reinterpret_cast<const float4*>(at), d1 = *reinterpret_cast<const float4*>(at + 16);
-            const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-            const uint32_t ug[4] = {zg.x, zg.y, zg.z, zg.w}, uu[4] = {zu.x, zu.y, zu.z, zu.w};
-            float dg[8], du[8], ac[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float gv = __uint_as_float((i & 1) ? ug[i / 2] & 0xffff0000u : ug[i / 2] << 16);
-                const float uv = __uint_as_float((i & 1) ? uu[i / 2] & 0xffff0000u : uu[i / 2] << 16);
-                const float s = 1.0f / (1.0f + __expf(-gv));
-                const float gs = gv * s;
-                du[i] = d[i] * gs;
-                ac[i] = gs * uv;
-                dg[i] = d[i] * uv * s * (1.0f + gv * (1.0f - s));
+            for (int j = 2 * jh; j < 2 * jh + 2; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    char* at = mine + (lane & 31) * kRow + (32 * (j & 1) + 8 * v + 4 * (lane >> 5)) * kElem;
+                    const float x0 = acc[i][j][4 * v], x1 = acc[i][j][4 * v + 1], x2 = acc[i][j][4 * v + 2],
+                                x3 = acc[i][j][4 * v + 3];
+                    if constexpr (SILU)
+                        *reinterpret_cast<float4*>(at) = make_float4(x0, x1, x2, x3);
+                    else
+                        *reinterpret_cast<uint2*>(at) = uint2{pack_bf2(x0, x1), pack_bf2(x2, x3)};
+                }
+            if (col >= K) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = 8 * q + (lane >> 3);
+                if (r >= rows) continue;
+                const char* at = mine + r * kRow + c8 * kElem;
+                if constexpr (SILU) {
+                    const float4 d0 = *reinterpret_cast<const float4*>(at), d1 = *reinterpret_cast<const float4*>(at + 16);
+                    const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+                    const uint32_t ug[4] = {zg[q].x, zg[q].y, zg[q].z, zg[q].w}, uu[4] = {zu[q].x, zu[q].y, zu[q].z, zu[q].w};
+                    float dg[8], du[8], ac[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float gv = __uint_as_float((x & 1) ? ug[x / 2] & 0xffff0000u : ug[x / 2] << 16);
+                        const float uv = __uint_as_float((x & 1) ? uu[x / 2] & 0xffff0000u : uu[x / 2] << 16);
+                        const float s = 1.0f / (1.0f + __expf(-gv));
+                        const float gs = gv * s;
+                        du[x] = d[x] * gs;
+                        ac[x] = gs * uv;
+                        dg[x] = d[x] * uv * s * (1.0f + gv * (1.0f - s));
+                    }
+                    uint16_t* o = static_cast<uint16_t*>(g.out) + p[q] * 2 * K + col;
+                    *reinterpret_cast<uint4*>(o) = uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])};
+                    *reinterpret_cast<uint4*>(o + K) = uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])};
+                    if (g.act)
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.act) + p[q] * K + col) =
+                            uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])};
+                } else {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p[q] * K + col) = *reinterpret_cast<const uint4*>(at);
+                }
             }
-            uint16_t* o = static_cast<uint16_t*>(g.out) + p * 2 * K + col;
-            *reinterpret_cast<uint4*>(o) = uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])};
-            *reinterpret_cast<uint4*>(o + K) = uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])};
-            if (g.act)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.act) + p * K + col) =
-                    uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])};
-        } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p * K + col) = *reinterpret_cast<const uint4*>(at);
         }
     }
 }
 
-template <int BM, bool SILU>
+template <int BM, bool SILU, bool NTW>
 static hipError_t launch_dx_t(const GradCall& c, hipStream_t s) {
     using C = DxCfg<BM>;
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dx_kernel<BM, SILU>),
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dx_kernel<BM, SILU, NTW>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::LdsBytes);
     if (attr != hipSuccess) return attr;
     const int m_tiles = (int)(moe_align_capacity(c.M, c.topk, c.E, BM) / BM), k_tiles = (c.K + 255) / 256;
     const int64_t nb = (int64_t)m_tiles * k_tiles;
     const int group = k_tiles <= 8 ? k_tiles : 2;
-    hipLaunchKernelGGL((grad_dx_kernel<BM, SILU>), dim3((unsigned)((nb + kXcds - 1) / kXcds * kXcds)), dim3(C::Threads),
+    hipLaunchKernelGGL((grad_dx_kernel<BM, SILU, NTW>), dim3((unsigned)((nb + kXcds - 1) / kXcds * kXcds)), dim3(C::Threads),
                        C::LdsBytes, s, c, m_tiles, k_tiles, group);
     return hipGetLastError();
 }
 
+template <int BM, bool SILU>
+static hipError_t launch_dx_w(const GradCall& c, hipStream_t s) {
+    return (long)c.M * c.topk <= 64L * c.E ? launch_dx_t<BM, SILU, true>(c, s) : launch_dx_t<BM, SILU, false>(c, s);
+}
+
 hipError_t launch_grad_dx(const GradCall& c, hipStream_t s) {
-    if (c.block_m == 128) return c.z ? launch_dx_t<128, true>(c, s) : launch_dx_t<128, false>(c, s);
-    return c.z ? launch_dx_t<64, true>(c, s) : launch_dx_t<64, false>(c, s);
+    if (c.block_m == 128) return c.z ? launch_dx_w<128, true>(c, s) : launch_dx_w<128, false>(c, s);
+    return c.z ? launch_dx_w<64, true>(c, s) : launch_dx_w<64, false>(c, s);
 }
 
 // ------------------------------------------------------------------------ dw
@@ -433,7 +459,8 @@ grad_dw_kernel(GradCall g, int n_tiles, int k_tiles, int per_xcd) {
         for (int q = 0; q < 32 * kLanes / 64; ++q) {
             const int r = q * (64 / kLanes) + lane / kLanes, n = n0 + wn * 64 + 32 * i + r;
             const uint4 v = *reinterpret_cast<const uint4*>(mine + r * kRow + (lane % kLanes) * 16);
-            if (n < N && col < K) *reinterpret_cast<uint4*>(out + ((size_t)n * K + col) * kElem) = v;
+            if (n < N && col < K)
+                __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(out + ((size_t)n * K + col) * kElem));
         }
     }
 }
