@@ -194,7 +194,7 @@ moe_status moe_align(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E
  *  kind = MOE_GEMM_GATE_UP (MOE_BF16): a = x [M][K=H], w = W1 [E][N=2I][K],
  *         c = z [P][N] bfloat16, gate columns 0..I-1 and up columns I..2I-1:
  *         what a backward pass through SiLU-and-mul needs (moe_grouped_gemm_dx).
- *         block_m 64 or 128; x or one expert's weights of 4 GiB or more ->
+ *         block_m 64 or 128; one expert's weights of 4 GiB or more ->
  *         MOE_ERR_UNSUPPORTED.
  *  dtype: MOE_F32 (a, w, c float32), MOE_BF16 (a, w, c bfloat16),
  *         MOE_FP8_E4M3 (w e4m3 with w_scale[E] float32 per expert matrix;

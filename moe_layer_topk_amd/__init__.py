@@ -92,7 +92,8 @@ def _layer_dtype(w: torch.Tensor, w_scale) -> int:
 
 def _call(fn, what: str, dev, *args) -> None:
     """fn(*args) with dev the current device (the library launches on it)."""
-    if dev.index == torch.cuda.current_device():
+    # (0.1 us a call; torch.cuda.current_device's own checks make it 0.3)
+    if dev.index == torch._C._cuda_getDevice():
         check(fn(*args), what)
     else:
         with torch.cuda.device(dev):
@@ -294,6 +295,7 @@ def _check_align(al: dict, P: int, E: int, dev, block_m=None) -> None:
 
 _BF16 = (torch.bfloat16,)
 _ROWS = (torch.float32, torch.bfloat16)
+_I32 = (torch.int32,)
 _GRAD_KINDS = (MOE_GEMM_GATE_UP, MOE_GEMM_DOWN)
 
 
@@ -385,7 +387,7 @@ def _rows_shape(name, rows, pair_row, weights, topk):
     nrows, H = rows.shape
     if pair_row is not None:
         M, k = pair_row.shape
-        _need("pair_row", pair_row, (torch.int32,), (M, k), rows.device)
+        _need("pair_row", pair_row, _I32, (M, k), rows.device)
     else:
         k = weights.shape[1] if weights is not None else topk
         if k is None or k < 1:
@@ -406,24 +408,27 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, al: dict, weights=None,
     (rows past the padded total are left as they were).  weights: float32 [M, k] or
     None.  Returns (rows, pair_row int32 [M, k]: the row of each pair, -1 for an id
     that is no expert)."""
-    M, H = x.shape
+    M, H = shape = x.shape
     topk = topk_ids.shape[1]
     dev = x.device
     stream = _stream(x)
-    E, cap = al["expert_counts"].numel(), moe_align_capacity(M, topk, al["expert_counts"].numel(), al["block_m"])
-    _need("x", x, _ROWS, (M, H), dev)
-    _need("topk_ids", topk_ids, (torch.int32,), (M, topk), dev)
+    E, block_m, P = al["expert_counts"].numel(), al["block_m"], M * topk
+    cap = -(-(P + min(E, P) * (block_m - 1)) // block_m) * block_m  # moe_align_capacity
+    _need("x", x, _ROWS, shape, dev)
+    _need("topk_ids", topk_ids, _I32, (M, topk), dev)
     _row_weights(weights, M, topk, dev)
-    _check_align(al, M * topk, E, dev)
+    _check_align(al, P, E, dev)
     if rows is None:
         rows = torch.empty((cap, H), dtype=x.dtype, device=dev)
+    else:
+        _need("rows", rows, (x.dtype,), (cap, H), dev)
     if pair_row is None:
         pair_row = torch.empty((M, topk), dtype=torch.int32, device=dev)
-    _need("rows", rows, (x.dtype,), (cap, H), dev)
-    _need("pair_row", pair_row, (torch.int32,), (M, topk), dev)
+    else:
+        _need("pair_row", pair_row, _I32, (M, topk), dev)
     bufs = align_struct(al)
     _call(lib().moe_permute, "moe_permute", dev, _DTYPES[x.dtype], x.data_ptr(), _p(weights), topk_ids.data_ptr(),
-          ctypes.byref(bufs), M, topk, E, al["block_m"], H, rows.data_ptr(), pair_row.data_ptr(), stream)
+          ctypes.byref(bufs), M, topk, E, block_m, H, rows.data_ptr(), pair_row.data_ptr(), stream)
     return rows, pair_row
 
 
@@ -436,7 +441,8 @@ def moe_unpermute(rows: torch.Tensor, pair_row=None, weights=None, topk=None, ou
     k, M, nrows, H = _rows_shape("rows", rows, pair_row, weights, topk)
     if out is None:
         out = torch.empty((M, H), dtype=rows.dtype if out_dtype is None else out_dtype, device=dev)
-    _need("out", out, _ROWS if out_dtype is None else (out_dtype,), (M, H), dev)
+    else:
+        _need("out", out, _ROWS if out_dtype is None else (out_dtype,), (M, H), dev)
     _call(lib().moe_unpermute, "moe_unpermute", dev, _DTYPES[rows.dtype], rows.data_ptr(), nrows, _p(pair_row), _p(weights),
           M, k, H, moe_dtype(out), out.data_ptr(), stream)
     return out
@@ -455,7 +461,7 @@ def moe_unpermute_backward(dout: torch.Tensor, rows, weights, pair_row=None, al=
     stream = _stream(dout)
     if pair_row is not None:
         k = pair_row.shape[1]
-        _need("pair_row", pair_row, (torch.int32,), (M, k), dev)
+        _need("pair_row", pair_row, _I32, (M, k), dev)
     else:
         k = weights.shape[1] if weights is not None else topk
         if k is None or k < 1:
@@ -524,25 +530,32 @@ def moe_permute_backward(drows: torch.Tensor, pair_row=None, x=None, weights=Non
 
 def _norm_spec(h, y, post_weight, gate, scale, pre_weight, eps):
     """(moe_norm_spec, gate of [M, 1]) for rows h [M, H], its weights checked."""
-    M, H = h.shape
-    dev = h.device
-    _need("h", h, _ROWS, (M, H), dev)
+    M, H = shape = h.shape
+    dev, dt = h.device, h.dtype
+    _need("h", h, _ROWS, shape, dev)
+    wdt = per_token = None
+    pw = pg = pp = None
     if y is not None:
-        _need("y", y, (h.dtype,), (M, H), dev)
+        _need("y", y, (dt,), shape, dev)
+        if post_weight is not None:
+            wdt = (post_weight.dtype,)
+            _need("post_weight", post_weight, wdt, (H,), dev)
+            pw = post_weight.data_ptr()
+        if gate is not None:
+            per_token = gate.dim() == 2
+            wdt = wdt or (gate.dtype,)
+            _need("gate", gate, wdt, (M, 1) if per_token else (H,), dev)
+            pg = gate.data_ptr()
     elif post_weight is not None or gate is not None:
         raise ValueError("post_weight and gate are a block's: they need y")
-    given = [t for t in (post_weight, gate, pre_weight) if t is not None]
-    wdt = given[0].dtype if given else h.dtype
+    if pre_weight is not None:
+        wdt = wdt or (pre_weight.dtype,)
+        _need("pre_weight", pre_weight, wdt, (H,), dev)
+        pp = pre_weight.data_ptr()
+    wdt = dt if wdt is None else wdt[0]
     if wdt not in _ROWS:
         raise ValueError(f"the norms' weights are {wdt}, expected torch.float32 or torch.bfloat16")
-    per_token = gate is not None and gate.dim() == 2
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if t is not None:
-            _need(name, t, (wdt,), (H,), dev)
-    if gate is not None:
-        _need("gate", gate, (wdt,), (M, 1) if per_token else (H,), dev)
-    return NormSpec(*(None if t is None else t.data_ptr() for t in (post_weight, gate, pre_weight)), _DTYPES[wdt],
-                    int(per_token), scale, eps), per_token
+    return NormSpec(pw, pg, pp, _DTYPES[wdt], 1 if per_token else 0, scale, eps), per_token
 
 
 def moe_residual_norm(h: torch.Tensor, y=None, post_weight=None, gate=None, scale: float = 1.0, pre_weight=None,
@@ -562,13 +575,16 @@ def moe_residual_norm(h: torch.Tensor, y=None, post_weight=None, gate=None, scal
         raise ValueError("without y, h_out is h")
     if pre_weight is None and x is not None:
         raise ValueError("x needs pre_weight")
-    if y is not None and h_out is None:
-        h_out = torch.empty_like(h)
-    if pre_weight is not None and x is None:
-        x = torch.empty_like(h)
-    for name, t in (("h_out", h_out), ("x", x)):
-        if t is not None:
-            _need(name, t, (h.dtype,), (M, H), dev)
+    if y is not None:
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        else:
+            _need("h_out", h_out, (h.dtype,), (M, H), dev)
+    if pre_weight is not None:
+        if x is None:
+            x = torch.empty_like(h)
+        else:
+            _need("x", x, (h.dtype,), (M, H), dev)
     _call(lib().moe_residual_norm, "moe_residual_norm", dev, _DTYPES[h.dtype], h.data_ptr(), _p(y), ctypes.byref(spec), M,
           H, _p(h_out), _p(x), stream)
     return (h if y is None else h_out), x

@@ -754,11 +754,11 @@ gemm_prefill2_kernel(GemmArgs g, int m_tiles, int n_tiles, int group_n) {
         const int r = (wave * C::ALoads + j) * C::RowsPerLoad + lrow;
         int p = g.sorted[mtile * C::BM + r];
         if (p >= P) p = g.sorted[mtile * C::BM];  // padding row: any valid row (its output is dropped)
-        const int src = (KIND != MOE_GEMM_DOWN) ? p / g.topk : p;
+        const int src = (KIND == MOE_GEMM_GATE_UP_SILU) ? p / g.topk : p;
         asrc[j] = (unsigned)((size_t)src * rowb + C::swz(lphys, r) * 16);
     }
-    // A: the tokens (GATE_UP kinds, P / topk rows) or the intermediate (DOWN, P rows)
-    const size_t arows = (KIND != MOE_GEMM_DOWN) ? (size_t)(P / g.topk) : (size_t)P;
+    // A: the tokens (GATE_UP, P / topk rows) or the intermediate (DOWN, P rows)
+    const size_t arows = (KIND == MOE_GEMM_GATE_UP_SILU) ? (size_t)(P / g.topk) : (size_t)P;
     const v4i_rsrc arsrc = buf_rsrc(g.a, (unsigned)(arows * rowb));
     const char* wbase = reinterpret_cast<const char*>(g.w) + (size_t)e * N * rowb;
     const v4i_rsrc brsrc = buf_rsrc(wbase, (unsigned)((size_t)N * rowb));  // this expert's N weight rows
@@ -2315,12 +2315,6 @@ hipError_t launch_grouped_gemm(const GemmCall& c, hipStream_t s) {
     a.amax_parts = c.amax_parts;
     a.amax_nparts = c.amax_nparts;
     const int64_t cap = moe_align_capacity(c.M, c.topk, c.E, c.block_m);
-    if (c.kind == MOE_GEMM_GATE_UP) {
-        // the plain product of token rows (kept for a backward pass): always the
-        // ring tile kernel, which the caller's checks leave nothing else for
-        if (c.block_m == PrefillCfg::BM) return launch_prefill2<MOE_GEMM_GATE_UP, MOE_BF16, PrefillCfg>(a, cap, c.E, s);
-        return launch_prefill2<MOE_GEMM_GATE_UP, MOE_BF16, PrefillCfg64>(a, cap, c.E, s);
-    }
     if (c.kind == MOE_GEMM_GATE_UP_SILU) return launch_kind<MOE_GEMM_GATE_UP_SILU>(c, a, cap, s);
     return launch_kind<MOE_GEMM_DOWN>(c, a, cap, s);
 }

@@ -1,5 +1,7 @@
-// Gradients of the grouped expert products, bfloat16 operands, float32 sums:
+// The grouped expert products as a training step needs them, bfloat16 operands,
+// float32 sums:
 //
+//   z:   z[p][n]     = sum_k x[p / topk][k] W[e][n][k]      (MOE_GEMM_GATE_UP)
 //   dx:  da[p][k]    = sum_n dc[p][n] W[e][n][k]            (rows of expert e)
 //        through SiLU-and-mul, with (g, u) the kept products z[p] and d = da[p]:
 //        dg = d u s (1 + g (1 - s)),  du = d g s,  act = g s u,  s = 1 / (1 + exp(-g))
@@ -56,35 +58,46 @@ __device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
 
 // ------------------------------------------------------------------------ dx
 //
-// Block tile BM rows (of one expert's run) x 256 columns k, 64 terms n a stage in
-// a ring of three; four wavefronts of BM/2 x 128.  W's columns are the matrix
-// instruction's rows, so a lane ends up with four consecutive k of a token.
+// Block tile BM rows (of one expert's run) x 256 output columns, 32 terms of the sum
+// a stage in a ring of three; four wavefronts of BM/2 x 128.  The weights are the
+// matrix instruction's rows, so a lane ends up with four consecutive columns of a
+// token.  kZ is the product itself, whose weights need no transposing.
+//
+// The gradients take 32 terms a stage, so that two workgroups fit a CU: one multiplies
+// while the other starts, waits at a barrier or writes out (down product of 8 experts
+// of 4096 x 14336, 8192 rows: 1480 -> 1285 us against 64 terms and one workgroup).  kZ
+// takes 64: its weight rows are read 128 bytes at a time, whole lines, instead of 64
+// (128 experts of 1536 x 2048, 16392 rows: 235 us against 270).
+enum DxMode { kDx, kDxSilu, kZ };
 
-template <int BM>
+template <int BM, int NS_>
 struct DxCfg {
-    static constexpr int ST = 3, Threads = 256, NS = 32;  // NS: terms n a stage
+    static constexpr int ST = 3, Threads = 256, NS = NS_;  // NS: terms of the sum a stage
+    static constexpr int Chunks = NS / 8;                  // 16-byte pieces of a row
     static constexpr int ABytes = BM * NS * 2, WBytes = NS * 512, StageBytes = ABytes + WBytes;
-    static constexpr int ALoads = BM / 16 / 4, WLoads = NS / 8, L = ALoads + WLoads;  // copies a wave and stage
+    static constexpr int RowsLoad = 64 / Chunks;           // rows a copy
+    static constexpr int ALoads = BM / RowsLoad / 4, WLoads = NS / 8, L = ALoads + WLoads;  // copies a wave and stage
     static constexpr int TM = BM / 64, TN = 4;
     static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + BM * 4;
-    // chunk c of 16 bytes of row r (rows of 64 bytes)
-    __device__ static __forceinline__ int swz(int c, int r) { return c ^ ((r >> 2) & 3); }
+    // place of piece c of row r: rows that share 256 bytes differ
+    __device__ static __forceinline__ int swz(int c, int r) { return c ^ ((r / (16 / Chunks)) % Chunks); }
 };
 
-template <int BM, bool SILU, bool NTW>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
-grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
-    using C = DxCfg<BM>;
+template <int BM, int MODE, bool NTW, int NS>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NS == 32 ? 2 : 1, 2)))
+grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
+    using C = DxCfg<BM, NS>;
+    constexpr bool SILU = MODE == kDxSilu;
     extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
-    const int nb = m_tiles * k_tiles;
+    const int nb = m_tiles * o_tiles;
     const int per = (nb + kXcds - 1) / kXcds;
     const int t = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
     if (t >= nb) return;
     // groups of `group` weight tiles; inside a group the row tiles advance slowest
     const int ng = t / (group * m_tiles);
-    const int gw = min(group, k_tiles - ng * group);
+    const int gw = min(group, o_tiles - ng * group);
     const int rem = t - ng * group * m_tiles;
-    const int mtile = rem / gw, ktile = ng * group + rem % gw;
+    const int mtile = rem / gw, otile = ng * group + rem % gw;
     const int e = g.al.tile_expert[mtile];
     if (e < 0) return;
 
@@ -92,28 +105,37 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int N = g.N, K = g.K, P = g.M * g.topk;
-    const int k0 = ktile * 256;
+    const int S = MODE == kZ ? K : N, O = MODE == kZ ? N : K;  // length of the sum, output columns
+    const int o0 = otile * 256;
     const int32_t* sorted = g.al.sorted_ids + (size_t)mtile * BM;
     int* ids_s = reinterpret_cast<int*>(grad_lds + C::IdsOffset);
     for (int i = tid; i < BM; i += C::Threads) ids_s[i] = sorted[i];
 
-    // sources of this wave's copies: rows of dc, and rows n of W (512 of their bytes)
+    // sources of this wave's copies: rows of dc (kZ: of x), and of W 32 rows n (512 of
+    // their bytes; kZ: 256 rows, 64 bytes)
     const char* asrc[C::ALoads];
 #pragma unroll
     for (int j = 0; j < C::ALoads; ++j) {
-        const int r = (wave * C::ALoads + j) * 16 + (lane >> 2);
+        const int r = (wave * C::ALoads + j) * C::RowsLoad + lane / C::Chunks;
         int p = sorted[r];
         if ((unsigned)p >= (unsigned)P) p = sorted[0];  // padding: any row, its results are dropped
-        asrc[j] = static_cast<const char*>(g.dc) + (size_t)p * N * 2 + C::swz(lane & 3, r) * 16;
+        if (MODE == kZ) p /= g.topk;
+        asrc[j] = static_cast<const char*>(g.dc) + (size_t)p * S * 2 + C::swz(lane % C::Chunks, r) * 16;
     }
-    // (columns past K read the next row, past the last row zeros; they are dropped)
+    // (columns past the last read the next row, past the last row zeros; they are dropped)
     const v4i_rsrc wrsrc = buf_rsrc(static_cast<const char*>(g.w) + (size_t)e * N * K * 2, (unsigned)((size_t)N * K * 2));
     unsigned wsrc[C::WLoads];
 #pragma unroll
     for (int j = 0; j < C::WLoads; ++j) {
-        const int r = (wave * C::WLoads + j) * 2 + (lane >> 5), c = lane & 31;
-        wsrc[j] = (unsigned)(((size_t)r * K + k0) * 2) + (tr_place(c >> 1, r) * 2 + (c & 1)) * 16;
+        if constexpr (MODE == kZ) {
+            const int r = (wave * C::WLoads + j) * C::RowsLoad + lane / C::Chunks;
+            wsrc[j] = (unsigned)((size_t)(o0 + r) * K * 2) + C::swz(lane % C::Chunks, r) * 16;
+        } else {
+            const int r = (wave * C::WLoads + j) * 2 + (lane >> 5), c = lane & 31;
+            wsrc[j] = (unsigned)(((size_t)r * K + o0) * 2) + (tr_place(c >> 1, r) * 2 + (c & 1)) * 16;
+        }
     }
+    const unsigned wstep = MODE == kZ ? C::NS * 2 : (unsigned)C::NS * 2 * K;  // bytes from a stage to the next
     const unsigned lds0 = lds_addr_of(grad_lds);
     auto issue_part = [&](int kt, int j0, int j1) {
         const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
@@ -123,10 +145,10 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
             if (j < C::ALoads)
                 lds_dma16_at(asrc[j] + (size_t)kt * (C::NS * 2), st + (wave * C::ALoads + j) * 1024);
             else if constexpr (NTW)
-                lds_dma16_buf_nt(wrsrc, wsrc[j - C::ALoads], (unsigned)((size_t)kt * (C::NS * 2) * K),
+                lds_dma16_buf_nt(wrsrc, wsrc[j - C::ALoads], kt * wstep,
                                  st + C::ABytes + (wave * C::WLoads + (j - C::ALoads)) * 1024);
             else
-                lds_dma16_buf(wrsrc, wsrc[j - C::ALoads], (unsigned)((size_t)kt * (C::NS * 2) * K),
+                lds_dma16_buf(wrsrc, wsrc[j - C::ALoads], kt * wstep,
                               st + C::ABytes + (wave * C::WLoads + (j - C::ALoads)) * 1024);
         }
     };
@@ -143,12 +165,13 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
     for (int i = 0; i < C::TM; ++i) arow[i] = wm * (BM / 2) + 32 * i + (lane & 31);
     unsigned wlane[C::TN];
 #pragma unroll
-    for (int j = 0; j < C::TN; ++j) wlane[j] = C::ABytes + tr_lane(lane, wn * 128 + 32 * j);
+    for (int j = 0; j < C::TN; ++j)
+        wlane[j] = C::ABytes + (MODE == kZ ? (wn * 128 + 32 * j + (lane & 31)) * (C::NS * 2) : tr_lane(lane, wn * 128 + 32 * j));
     // 32-row groups of the tile that hold no pair are left out
     const int nreal = min(BM, g.al.expert_offsets[e] + g.al.expert_counts[e] - mtile * BM);
     const int live = __builtin_amdgcn_readfirstlane(min(C::TM, max(0, (nreal - wm * (BM / 2) + 31) / 32)));
 
-    const int nk = N / C::NS;
+    const int nk = S / C::NS;
 #pragma unroll
     for (int s0 = 0; s0 < C::ST - 1; ++s0)
         if (s0 < nk) issue_part(s0, 0, C::L);
@@ -170,7 +193,12 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
                 af[buf][i] = *reinterpret_cast<const bf16x8*>(sa + arow[i] * (C::NS * 2) + (C::swz(c, arow[i]) << 4));
 #pragma unroll
             for (int j = 0; j < C::TN; ++j)
-                if (LT) wf[buf][j] = tr_read8(st + wlane[j] + ks * 16 * 512);
+                if constexpr (LT > 0) {
+                    if constexpr (MODE == kZ)
+                        wf[buf][j] = *reinterpret_cast<const bf16x8*>(sa + wlane[j] + (C::swz(c, lane & 31) << 4));
+                    else
+                        wf[buf][j] = tr_read8(st + wlane[j] + ks * 16 * 512);
+                }
         };
         read_frags(0, 0);
 #pragma unroll
@@ -219,16 +247,16 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
         const int r0 = wm * (BM / 2) + 32 * i, rows = min(32, nreal - r0);
 #pragma unroll
         for (int jh = 0; jh < 2; ++jh) {
-            const int col = k0 + wn * 128 + 64 * jh + c8;
+            const int col = o0 + wn * 128 + 64 * jh + c8;
             size_t p[4];
             uint4 zg[4], zu[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int r = 8 * q + (lane >> 3);
                 p[q] = (size_t)ids_s[r0 + min(r, rows - 1)];
-                if (SILU && col < K) {
-                    const uint16_t* z = static_cast<const uint16_t*>(g.z) + p[q] * 2 * K + col;
-                    zg[q] = *reinterpret_cast<const uint4*>(z), zu[q] = *reinterpret_cast<const uint4*>(z + K);
+                if (SILU && col < O) {
+                    const uint16_t* z = static_cast<const uint16_t*>(g.z) + p[q] * 2 * O + col;
+                    zg[q] = *reinterpret_cast<const uint4*>(z), zu[q] = *reinterpret_cast<const uint4*>(z + O);
                 }
             }
 #pragma unroll
@@ -243,7 +271,7 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
                     else
                         *reinterpret_cast<uint2*>(at) = uint2{pack_bf2(x0, x1), pack_bf2(x2, x3)};
                 }
-            if (col >= K) continue;
+            if (col >= O) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int r = 8 * q + (lane >> 3);
@@ -264,43 +292,51 @@ grad_dx_kernel(GradCall g, int m_tiles, int k_tiles, int group) {
                         ac[x] = gs * uv;
                         dg[x] = d[x] * uv * s * (1.0f + gv * (1.0f - s));
                     }
-                    uint16_t* o = static_cast<uint16_t*>(g.out) + p[q] * 2 * K + col;
+                    uint16_t* o = static_cast<uint16_t*>(g.out) + p[q] * 2 * O + col;
                     *reinterpret_cast<uint4*>(o) = uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])};
-                    *reinterpret_cast<uint4*>(o + K) = uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])};
+                    *reinterpret_cast<uint4*>(o + O) = uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])};
                     if (g.act)
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.act) + p[q] * K + col) =
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.act) + p[q] * O + col) =
                             uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])};
                 } else {
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p[q] * K + col) = *reinterpret_cast<const uint4*>(at);
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p[q] * O + col) = *reinterpret_cast<const uint4*>(at);
                 }
             }
         }
     }
 }
 
-template <int BM, bool SILU, bool NTW>
+template <int BM, int MODE, bool NTW, int NS>
 static hipError_t launch_dx_t(const GradCall& c, hipStream_t s) {
-    using C = DxCfg<BM>;
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dx_kernel<BM, SILU, NTW>),
+    using C = DxCfg<BM, NS>;
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dx_kernel<BM, MODE, NTW, NS>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, C::LdsBytes);
     if (attr != hipSuccess) return attr;
-    const int m_tiles = (int)(moe_align_capacity(c.M, c.topk, c.E, BM) / BM), k_tiles = (c.K + 255) / 256;
-    const int64_t nb = (int64_t)m_tiles * k_tiles;
-    const int group = k_tiles <= 8 ? k_tiles : 2;
-    hipLaunchKernelGGL((grad_dx_kernel<BM, SILU, NTW>), dim3((unsigned)((nb + kXcds - 1) / kXcds * kXcds)), dim3(C::Threads),
-                       C::LdsBytes, s, c, m_tiles, k_tiles, group);
+    const int m_tiles = (int)(moe_align_capacity(c.M, c.topk, c.E, BM) / BM), o_tiles = ((MODE == kZ ? c.N : c.K) + 255) / 256;
+    const int64_t nb = (int64_t)m_tiles * o_tiles;
+    // weight tiles a group: all of few; an XCD's share where they divide (the down
+    // product's 56: 7 1232-1264 us, 2 1256-1284, 4 1279-1300, 8 1298-1339), else 2
+    const int group = o_tiles <= 8 ? o_tiles : o_tiles % kXcds == 0 && o_tiles <= 64 ? o_tiles / kXcds : 2;
+    hipLaunchKernelGGL((grad_dx_kernel<BM, MODE, NTW, NS>), dim3((unsigned)((nb + kXcds - 1) / kXcds * kXcds)), dim3(C::Threads),
+                       C::LdsBytes, s, c, m_tiles, o_tiles, group);
     return hipGetLastError();
 }
 
-template <int BM, bool SILU>
+template <int BM, int MODE>
 static hipError_t launch_dx_w(const GradCall& c, hipStream_t s) {
-    return (long)c.M * c.topk <= 64L * c.E ? launch_dx_t<BM, SILU, true>(c, s) : launch_dx_t<BM, SILU, false>(c, s);
+    return (long)c.M * c.topk <= 64L * c.E ? launch_dx_t<BM, MODE, true, MODE == kZ ? 64 : 32>(c, s) : launch_dx_t<BM, MODE, false, MODE == kZ ? 64 : 32>(c, s);
+}
+
+template <int MODE>
+static hipError_t launch_dx_m(const GradCall& c, hipStream_t s) {
+    return c.block_m == 128 ? launch_dx_w<128, MODE>(c, s) : launch_dx_w<64, MODE>(c, s);
 }
 
 hipError_t launch_grad_dx(const GradCall& c, hipStream_t s) {
-    if (c.block_m == 128) return c.z ? launch_dx_w<128, true>(c, s) : launch_dx_w<128, false>(c, s);
-    return c.z ? launch_dx_w<64, true>(c, s) : launch_dx_w<64, false>(c, s);
+    return c.z ? launch_dx_m<kDxSilu>(c, s) : launch_dx_m<kDx>(c, s);
 }
+
+hipError_t launch_gate_up(const GradCall& c, hipStream_t s) { return launch_dx_m<kZ>(c, s); }
 
 // ------------------------------------------------------------------------ dw
 //

@@ -10,6 +10,7 @@
 
 #include "moe_fused.h"
 #include "moe_launch.h"
+#include "moe_train.h"
 
 using namespace moe;
 
@@ -262,9 +263,8 @@ moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, 
     if (N < 1 || K < 1 || N % 128 || K % 128) return MOE_ERR_SHAPE;
     if ((kind == MOE_GEMM_GATE_UP_SILU || kind == MOE_GEMM_GATE_UP) && N % 256) return MOE_ERR_SHAPE;
     if (!valid_block_m(block_m)) return MOE_ERR_UNSUPPORTED;
-    // (the tile kernel's rows and 32-bit offsets into its operands)
-    if (kind == MOE_GEMM_GATE_UP &&
-        (!prefill_supported_block_m(block_m) || (uint64_t)M * K * 2 > 0xffffffffull || (uint64_t)N * K * 2 > 0xffffffffull))
+    // (32-bit offsets into an expert's weights)
+    if (kind == MOE_GEMM_GATE_UP && (!prefill_supported_block_m(block_m) || (uint64_t)N * K * 2 > 0xffffffffull))
         return MOE_ERR_UNSUPPORTED;
     const bool fp8 = dtype == MOE_FP8_E4M3, w4 = dtype == MOE_W4A16;
     if ((fp8 || w4) && K % 256) return MOE_ERR_SHAPE;
@@ -277,6 +277,9 @@ moe_status moe_grouped_gemm(moe_gemm_kind kind, moe_dtype dtype, const void* a, 
     if (fp8 && (!a_scale || !w_scale || (kind == MOE_GEMM_GATE_UP_SILU && !c_amax))) return MOE_ERR_NULL;
     if (w4 && !w_scale) return MOE_ERR_NULL;
     if (misaligned(a) || misaligned(w) || misaligned(c) || misaligned(w_scale)) return MOE_ERR_ALIGNMENT;
+    if (kind == MOE_GEMM_GATE_UP)
+        return hip_status(launch_gate_up(GradCall{a, nullptr, w, nullptr, *al, M, topk, E, N, K, block_m, true, MOE_BF16, c, nullptr},
+                                         static_cast<hipStream_t>(stream)));
     GemmCall g{kind, dtype, a, a_scale, w, w_scale, *al, M, topk, E, N, K, block_m, c, c_amax, 1, nullptr, act_q8};
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (fp8 && kind == MOE_GEMM_GATE_UP_SILU) {

@@ -68,9 +68,9 @@ struct NormGrad {
 int norm_grad_groups(int M, int H);
 hipError_t launch_residual_norm_backward(const NormGrad& c, hipStream_t s);
 
-// Gradients of the grouped products (bfloat16 operands).
+// The grouped products' gradients, and the plain product of token rows (bfloat16).
 struct GradCall {
-    const void* dc;  // [P][N] pair order
+    const void* dc;  // [P][N] pair order (gate_up: x [M][K])
     const void* a;   // dw: [M][K] (per token) or [P][K]
     const void* w;   // dx: [E][N][K]
     const void* z;   // dx through SiLU-and-mul: [P][2K]
@@ -81,6 +81,7 @@ struct GradCall {
     void* out;            // dx: [P][K], or [P][2K] with z; dw: [E][N][K]
     void* act;            // dx with z: [P][K] or NULL
 };
+hipError_t launch_gate_up(const GradCall& c, hipStream_t s);  // out [P][N]
 hipError_t launch_grad_dx(const GradCall& c, hipStream_t s);
 hipError_t launch_grad_dw(const GradCall& c, hipStream_t s);
 
