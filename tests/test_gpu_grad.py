@@ -226,6 +226,12 @@ def test_operands_past_four_gib(dev):
         d, v = dc[r].double(), w[0].double()
         want = d @ v
         close(da[r], want.cpu(), (HALF[BF] * want.abs() + 2 * N * U * (d.abs() @ v.abs())).cpu(), "da")
+    w1 = (torch.randn(1, 256, N, generator=g, device=dev) * 0.02).to(BF)
+    z, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP, dc, w1, al, M, 1)  # (dc as the tokens)
+    for r in (slice(0, 3), slice(M - 3, M)):
+        d, v = dc[r].double(), w1[0].double().t()
+        want = d @ v
+        close(z[r], want.cpu(), (HALF[BF] * want.abs() + 2 * N * U * (d.abs() @ v.abs())).cpu(), "z")
     dw = moe.moe_grouped_gemm_dw(moe.MOE_GEMM_DOWN, dc, a, al, M, 1, dtype=F32)
     for c in (slice(0, 3), slice(N - 3, N)):
         d, v = dc[:, c].double(), a.double()

@@ -176,7 +176,6 @@ def test_gate_up(L, bal):
     assert g(bm=16) == 3
     assert g(bm=256) == 3
     assert g(sa=FAKE) == 3
-    assert g(M=1 << 22, K=1024) == 3           # x reaches 4 GiB
     assert g(N=1 << 20, K=4096) == 3
     assert g(a=NULL) == 1
     assert g(c=ODD) == 5
