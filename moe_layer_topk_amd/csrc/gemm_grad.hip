@@ -89,10 +89,13 @@ grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
     using C = DxCfg<BM, NS>;
     constexpr bool SILU = MODE == kDxSilu;
     extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
+    // the row tiles that exist, cut into one range for each XCD (of those the grid allows
+    // for, a batch of few rows an expert leaves a third or more empty, at the end)
+    m_tiles = min(m_tiles, g.al.expert_offsets[g.E] / BM);
     const int nb = m_tiles * o_tiles;
     const int per = (nb + kXcds - 1) / kXcds;
-    const int t = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-    if (t >= nb) return;
+    const int l = blockIdx.x / kXcds, t = (blockIdx.x % kXcds) * per + l;
+    if (l >= per || t >= nb) return;
     // groups of `group` weight tiles; inside a group the row tiles advance slowest
     const int ng = t / (group * m_tiles);
     const int gw = min(group, o_tiles - ng * group);
@@ -439,30 +442,31 @@ grad_dw_kernel(GradCall g, int n_tiles, int k_tiles, int per_xcd) {
                 wait_vm_runtime<C::L>(min(C::ST - 2, nst - 1 - kt));
             __syncthreads();
             const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+            // the first half's fragments, then its products with the second half's reads and
+            // the copies between them: a wavefront that read both halves first kept the
+            // others' first reads waiting (3.88 -> 3.66 million cycles, 2060 -> 2022 us)
             bf16x8 nf[2][2], kf[2][4];
-            auto read = [&](int ks) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) nf[ks][i] = tr_read8(st + nlane[i] + ks * 16 * 512);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) kf[ks][j] = tr_read8(st + klane[j] + ks * 16 * 512);
+            auto read = [&](int ks, int m) {
+                if (m < 4)
+                    kf[ks][m] = tr_read8(st + klane[m] + ks * 16 * 512);
+                else
+                    nf[ks][m - 4] = tr_read8(st + nlane[m - 4] + ks * 16 * 512);
             };
-            read(0);
-            __builtin_amdgcn_sched_barrier(0);
-            read(1);
-            if (pf) issue(kt + C::ST - 1, 0);
+            constexpr int kOrder[6] = {4, 0, 1, 2, 3, 5};
+#pragma unroll
+            for (int m = 0; m < 6; ++m) read(0, kOrder[m]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                acc[q / 4][q % 4] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[0][q % 4], nf[0][q / 4], acc[q / 4][q % 4], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            if (pf) {
-                issue(kt + C::ST - 1, 1);
-                if (kt + C::ST < nst) fetch_ids(kt + C::ST);
+            for (int q = 0; q < 16; ++q) {
+                const int ks = q / 8, i = q / 4 % 2, j = q % 4;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[ks][j], nf[ks][i], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (q < 6) read(1, kOrder[q]);
+                if (pf && q == 1) issue(kt + C::ST - 1, 0);
+                if (pf && q == 5) issue(kt + C::ST - 1, 1);
+                if (pf && q == 12 && kt + C::ST < nst) fetch_ids(kt + C::ST);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                acc[q / 4][q % 4] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[1][q % 4], nf[1][q / 4], acc[q / 4][q % 4], 0, 0, 0);
         };
         const int nmain = max(0, nst - (C::ST - 1));
         for (int kt = 0; kt < nmain; ++kt) stage(kt, std::true_type{});
