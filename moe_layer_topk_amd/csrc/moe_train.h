@@ -63,7 +63,7 @@ struct NormGrad {
     int M, H;
     void *dh, *dy;
     float *dpost, *dgate, *dpre;
-    float* part;  // [norm_grad_groups(M, H)][3][H]
+    float* part;  // [norm_grad_groups(M, H)][2][H]
 };
 int norm_grad_groups(int M, int H);
 hipError_t launch_residual_norm_backward(const NormGrad& c, hipStream_t s);

@@ -183,7 +183,7 @@ __device__ __forceinline__ void store_part(float* x, const float (&v)[E]) {
 }
 
 // The rows a thread of the gradient kernel reads: its columns of h', dx, dh' and y.
-template <int DT, int T, int V>
+template <int DT, int T, int V, bool FULL>
 struct GradRow {
     Raw<DT> h[V], dx[V], dh[V], y[V];
     __device__ __forceinline__ void load(const NormGrad& c, int t, bool pre) {
@@ -191,6 +191,11 @@ struct GradRow {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = (i * T + (int)threadIdx.x) * Raw<DT>::E;
+            if constexpr (FULL) {
+                h[i].load(c.h_out, row + col), dx[i].load(c.dx, row + col);
+                dh[i].load(c.dh_out, row + col), y[i].load(c.y, row + col);
+                continue;
+            }
             const bool in = col < c.H;
             if (in && pre) h[i].load(c.h_out, row + col), dx[i].load(c.dx, row + col);
             else h[i].zero(), dx[i].zero();
@@ -204,158 +209,148 @@ struct GradRow {
 
 // Gradients.  With n = v r the normed row of v and q = d w the gradient at n,
 // the gradient of v is r (q - n mean(q n)), and w's is the sum over rows of d n.
-// A workgroup takes rows t, t + groups, ... and keeps its part of the three column
-// sums in registers; norm_parts_kernel adds the parts in order.  kHold: the weights
-// stay in registers; kNext: the next row is on its way while this one waits for its
-// sums (a row may be written over one of its inputs, never over another row's).
-template <int DT, int T, int V, bool kHold, bool kNext, int W>
+// At the block d = s dh' (times the token's gate), q = d g w_post, and one column sum
+// S = sum d n gives both dw_post = g S and dg = w_post S (a gate a column).
+//
+// A workgroup takes rows t, t + groups, ... and keeps its part of the two column sums
+// in registers; norm_parts_kernel adds the parts in order.  kHold: the weights stay in
+// registers and the next row is on its way while this one waits for its sums (a row
+// may be written over one of its inputs, never over another row's).  FULL: everything
+// is there (both norms' gradients and the stream's, no gate a token) and a row fills
+// the workgroup, so that no load or store hangs on a condition: with one pending, the
+// compiler waits for the next row and the stores too.  (The fused multiply-adds are
+// spelled out, so that both forms round alike.)
+template <int DT, int T, int V, int W, bool kHold, bool FULL>
 __global__ void __launch_bounds__(T, W) residual_norm_backward_kernel(NormGrad c) {
     __shared__ __attribute__((aligned(16))) float lds1[2][3][T / 64];
     __shared__ __attribute__((aligned(16))) float lds2[2][2][T / 64];
     constexpr int E = Raw<DT>::E;
     const int tid = threadIdx.x;
     const bool bf = c.n.w_dtype == MOE_BF16;
-    const bool pre = c.n.pre_weight != nullptr, post = c.n.post_weight != nullptr;
-    const bool gate_c = c.n.gate && !c.n.gate_per_token, gate_t = c.n.gate && c.n.gate_per_token;
+    const bool pre = FULL || c.n.pre_weight != nullptr, post = c.n.post_weight != nullptr;
+    const bool gate_c = c.n.gate && (FULL || !c.n.gate_per_token), gate_t = !FULL && c.n.gate && c.n.gate_per_token;
     const float inv_h = 1.0f / (float)c.H;
-    float wpre[kHold ? E * V : 1], wpost[kHold ? E * V : 1], wgate[kHold ? E * V : 1];
-    if constexpr (kHold) {
+    // w_pre, and w_post times the column's gate
+    auto load_weights = [&](int col, float* wpre, float* wq) {
+        float g[E];
 #pragma unroll
-        for (int k = 0; k < E * V; ++k) wpre[k] = wpost[k] = wgate[k] = 1.0f;
+        for (int k = 0; k < E; ++k) wpre[k] = wq[k] = g[k] = 1.0f;
+        if (pre) load_w<E>(c.n.pre_weight, bf, col, wpre);
+        if (post) load_w<E>(c.n.post_weight, bf, col, wq);
+        if (gate_c) load_w<E>(c.n.gate, bf, col, g);
+#pragma unroll
+        for (int k = 0; k < E; ++k) wq[k] *= g[k];
+    };
+    constexpr int VW = kHold ? V : 1;
+    float wpre[VW][E], wq[VW][E];
+    if constexpr (kHold) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = (i * T + tid) * E;
-            if (col >= c.H) continue;
-            if (pre) load_w<E>(c.n.pre_weight, bf, col, wpre + E * i);
-            if (post) load_w<E>(c.n.post_weight, bf, col, wpost + E * i);
-            if (gate_c) load_w<E>(c.n.gate, bf, col, wgate + E * i);
+#pragma unroll
+            for (int k = 0; k < E; ++k) wpre[i][k] = wq[i][k] = 0.0f;
+            if (FULL || col < c.H) load_weights(col, wpre[i], wq[i]);
         }
     }
-    float apost[V][E], agate[V][E], apre[V][E];
+    float apre[V][E], ablk[V][E];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int k = 0; k < E; ++k) apost[i][k] = agate[i][k] = apre[i][k] = 0.0f;
-    GradRow<DT, T, V> in, next;
-    if (kNext && (int)blockIdx.x < c.M) next.load(c, blockIdx.x, pre);
+        for (int k = 0; k < E; ++k) apre[i][k] = ablk[i][k] = 0.0f;
+    GradRow<DT, T, V, FULL> in, next;
+    if (kHold && (int)blockIdx.x < c.M) next.load(c, blockIdx.x, pre);
     int odd = 0;
     for (int t = blockIdx.x; t < c.M; t += gridDim.x, odd ^= 1) {
         const size_t row = (size_t)t * c.H;
-        if constexpr (kNext) {
+        if constexpr (kHold) {
             in = next;
             if (t + (int)gridDim.x < c.M) next.load(c, t + gridDim.x, pre);
         } else {
             in.load(c, t, pre);
         }
-        float dh[V][E];
         float s[3] = {0.0f, 0.0f, 0.0f};  // y^2, h'^2, dx w_pre h'
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = (i * T + tid) * E;
-            float w[E];
-            if constexpr (!kHold) {
-                if (pre && col < c.H) load_w<E>(c.n.pre_weight, bf, col, w);
-            }
+            if (!FULL && col >= c.H) continue;
+            if constexpr (!kHold) load_weights(col, wpre[0], wq[0]);
+            const float* w = wpre[kHold ? i : 0];
 #pragma unroll
             for (int k = 0; k < E; ++k) {
                 const float y = in.y[i].at(k), h = in.h[i].at(k);
-                dh[i][k] = in.dh[i].at(k);
                 s[0] = fmaf(y, y, s[0]);
-                if (pre && col < c.H) {
-                    s[1] = fmaf(h, h, s[1]);
-                    s[2] = fmaf(in.dx[i].at(k) * (kHold ? wpre[kHold ? E * i + k : 0] : w[k]), h, s[2]);
-                }
+                s[1] = fmaf(h, h, s[1]);
+                s[2] = fmaf(in.dx[i].at(k) * w[k], h, s[2]);
             }
         }
         group_sum<T, 3>(s, lds1[odd]);
-        const float r1 = post ? 1.0f / sqrtf(s[0] * inv_h + c.n.eps) : 1.0f;
-        if (pre) {
-            const float r2 = 1.0f / sqrtf(s[1] * inv_h + c.n.eps);
-            const float m = s[2] * r2 * inv_h;  // mean of q n
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int col = (i * T + tid) * E;
-                if (col >= c.H) continue;
-                float w[E];
-                if constexpr (!kHold) load_w<E>(c.n.pre_weight, bf, col, w);
-#pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    const float n = in.h[i].at(k) * r2;
-                    apre[i][k] = fmaf(in.dx[i].at(k), n, apre[i][k]);
-                    dh[i][k] += r2 * (in.dx[i].at(k) * (kHold ? wpre[kHold ? E * i + k : 0] : w[k]) - n * m);
-                }
-            }
-        }
+        const float r1 = post ? 1.0f / sqrtf(fmaf(s[0], inv_h, c.n.eps)) : 1.0f;
+        const float r2 = pre ? 1.0f / sqrtf(fmaf(s[1], inv_h, c.n.eps)) : 0.0f;
+        const float m2 = s[2] * r2 * inv_h;  // mean of q n at the second norm
+        const float gt = c.n.scale * (gate_t ? load1w(c.n.gate, bf, t) : 1.0f);
+        float s2[2] = {0.0f, 0.0f};  // q n at the first norm, s dh' u
+        float d[V][E];               // q there
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = (i * T + tid) * E;
-            if (col < c.H) Raw<DT>::store(c.dh, row + col, dh[i]);
-        }
-        if (!c.y) continue;
-        // du = s g dh'; through the post norm
-        float s2[2] = {0.0f, 0.0f};  // du w_post y r1, s dh' u
-        const float gt = gate_t ? load1w(c.n.gate, bf, t) : 1.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int col = (i * T + tid) * E;
-            if (col >= c.H) continue;
-            float w[E], g[E];
-            if constexpr (!kHold) {
-                if (post) load_w<E>(c.n.post_weight, bf, col, w);
-                if (gate_c) load_w<E>(c.n.gate, bf, col, g);
-            }
+            if (!FULL && col >= c.H) continue;
+            if constexpr (!kHold) load_weights(col, wpre[0], wq[0]);
+            const float *w = wpre[kHold ? i : 0], *v = wq[kHold ? i : 0];
+            float dh[E];
 #pragma unroll
             for (int k = 0; k < E; ++k) {
-                const float wp = kHold ? wpost[kHold ? E * i + k : 0] : post ? w[k] : 1.0f;
-                const float n = in.y[i].at(k) * r1, u = n * wp;
-                const float d = c.n.scale * dh[i][k];  // at g u
-                agate[i][k] = fmaf(d, u, agate[i][k]);
-                s2[1] = fmaf(d, u, s2[1]);
-                const float du = d * (gate_c ? (kHold ? wgate[kHold ? E * i + k : 0] : g[k]) : gt);
-                apost[i][k] = fmaf(du, n, apost[i][k]);
-                const float q = du * wp;
-                s2[0] = fmaf(q, n, s2[0]);
-                dh[i][k] = q;
+                const float n = in.h[i].at(k) * r2, x = in.dx[i].at(k);  // (no second norm: 0)
+                apre[i][k] = fmaf(x, n, apre[i][k]);
+                dh[k] = fmaf(r2, fmaf(-n, m2, x * w[k]), in.dh[i].at(k));
+            }
+            Raw<DT>::store(c.dh, row + col, dh);
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float n = in.y[i].at(k) * r1, e = gt * dh[k];
+                ablk[i][k] = fmaf(e, n, ablk[i][k]);
+                d[i][k] = e * v[k];
+                s2[0] = fmaf(d[i][k], n, s2[0]);
+                if (gate_t) s2[1] = fmaf(c.n.scale * dh[k] * v[k], n, s2[1]);
             }
         }
-        if (post || gate_t) group_sum<T, 2>(s2, lds2[odd]);
-        const float m = post ? s2[0] * inv_h : 0.0f;
+        if (!FULL && !c.y) continue;
+        if (FULL || post || gate_t) group_sum<T, 2>(s2, lds2[odd]);
+        const float m1 = post ? s2[0] * inv_h * r1 : 0.0f;
         if (gate_t && tid == 0 && c.dgate) c.dgate[t] = s2[1];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = (i * T + tid) * E;
-            if (col >= c.H) continue;
+            if (!FULL && col >= c.H) continue;
             float o[E];
 #pragma unroll
-            for (int k = 0; k < E; ++k) o[k] = post ? r1 * (dh[i][k] - in.y[i].at(k) * r1 * m) : dh[i][k];
+            for (int k = 0; k < E; ++k) o[k] = r1 * fmaf(-in.y[i].at(k), m1, d[i][k]);  // (no post norm: r1 = 1, m1 = 0)
             Raw<DT>::store(c.dy, row + col, o);
         }
     }
-    float* part = c.part + (size_t)blockIdx.x * 3 * c.H;
+    float* part = c.part + (size_t)blockIdx.x * 2 * c.H;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int col = (i * T + tid) * E;
-        if (col >= c.H) continue;
-        if (c.dpost) store_part(part + col, apost[i]);
-        if (c.dgate && gate_c) store_part(part + c.H + col, agate[i]);
-        if (c.dpre) store_part(part + 2 * c.H + col, apre[i]);
+        if (!FULL && col >= c.H) continue;
+        if (c.dpre) store_part(part + col, apre[i]);
+        if (c.dpost || (c.dgate && gate_c)) store_part(part + c.H + col, ablk[i]);
     }
 }
 
-// Sums of the groups' parts: blockIdx.y the vector; 16 lanes take 64 columns, 64
-// slices of the groups meet in LDS, all in a fixed order.
-__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* __restrict__ part, int groups, int H, float* dpost,
-                                                         float* dgate, float* dpre) {
+// Sums of the groups' parts: blockIdx.y 0 the second norm's weight, 1 the block's sum,
+// times the gate and the first norm's weight.  16 lanes take 64 columns, 64 slices of
+// the groups meet in LDS, all in a fixed order.
+__global__ void __launch_bounds__(1024) norm_parts_kernel(NormGrad c, int groups) {
     __shared__ float lds[64][64];
-    float* out = blockIdx.y == 0 ? dpost : blockIdx.y == 1 ? dgate : dpre;
-    if (!out) return;
-    const int slice = threadIdx.x >> 4, c4 = (threadIdx.x & 15) * 4, col = blockIdx.x * 64 + c4;
+    const bool pre = blockIdx.y == 0, bf = c.n.w_dtype == MOE_BF16;
+    if (pre ? !c.dpre : !c.dpost && !(c.dgate && !c.n.gate_per_token)) return;
+    const int H = c.H, slice = threadIdx.x >> 4, c4 = (threadIdx.x & 15) * 4, col = blockIdx.x * 64 + c4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < H) {
-        const float* p = part + (size_t)blockIdx.y * H + col;
+        const float* p = c.part + (size_t)blockIdx.y * H + col;
 #pragma unroll 8
         for (int g = slice; g < groups; g += 64) {
-            const float4 v = *reinterpret_cast<const float4*>(p + (size_t)g * 3 * H);
+            const float4 v = *reinterpret_cast<const float4*>(p + (size_t)g * 2 * H);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
     }
@@ -366,7 +361,13 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* __restric
         float t = 0.0f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) t += lds[i][threadIdx.x];
-        out[o] = t;
+        if (pre) {
+            c.dpre[o] = t;
+        } else {
+            const bool gate_c = c.n.gate && !c.n.gate_per_token;
+            if (c.dpost) c.dpost[o] = gate_c ? t * load1w(c.n.gate, bf, o) : t;
+            if (c.dgate && gate_c) c.dgate[o] = c.n.post_weight ? t * load1w(c.n.post_weight, bf, o) : t;
+        }
     }
 }
 
@@ -396,7 +397,7 @@ hipError_t launch_residual_norm(const NormCall& c, hipStream_t s) {
 
 // Workgroups of the gradient kernel: two of 512 threads a CU, as many threads of
 // smaller ones (at 4096 x 4096 512 45 us, 256 49, 768 53), but eight rows each where
-// there are rows enough, since every group leaves 12 bytes a column to be added.
+// there are rows enough, since every group leaves 8 bytes a column to be added.
 int norm_grad_groups(int M, int H) {
     const int most = H > 2048 ? 512 : 1024;
     const int g = M / 8 < 256 ? 256 : M / 8;
@@ -405,13 +406,20 @@ int norm_grad_groups(int M, int H) {
 
 template <int DT, int T, int V, int W, bool kHold>
 static hipError_t grad_tv(const NormGrad& c, int groups, hipStream_t s) {
-    hipLaunchKernelGGL((residual_norm_backward_kernel<DT, T, V, kHold, kHold, W>), dim3(groups), dim3(T), 0, s, c);
+    if constexpr (kHold) {
+        if (c.H == T * V * Raw<DT>::E && c.n.pre_weight && c.y && c.dh_out && !(c.n.gate && c.n.gate_per_token)) {
+            hipLaunchKernelGGL((residual_norm_backward_kernel<DT, T, V, W, true, true>), dim3(groups), dim3(T), 0, s, c);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((residual_norm_backward_kernel<DT, T, V, W, kHold, false>), dim3(groups), dim3(T), 0, s, c);
     return hipGetLastError();
 }
 
-// One 16-byte piece a thread, the weights and the next row in registers (4096 x
-// 4096 bfloat16 45 us; without the next row 47, without either 49; two pieces a
-// thread 47-97), until a workgroup has no more threads.
+// One 16-byte piece a thread, the weights and the next row in registers (4096 x 4096
+// bfloat16 with three column sums: 45 us, without the next row 47, without either 49,
+// two pieces a thread 47-97; FULL and two sums: 41 us, 4.9 TB/s, and 47 on inputs that
+// change from call to call), until a workgroup has no more threads.
 template <int DT>
 static hipError_t grad_dt(const NormGrad& c, int groups, hipStream_t s) {
     constexpr int E = Raw<DT>::E;
@@ -431,10 +439,9 @@ hipError_t launch_residual_norm_backward(const NormGrad& c, hipStream_t s) {
     const int groups = norm_grad_groups(c.M, c.H);
     hipError_t e = c.dtype == MOE_BF16 ? grad_dt<MOE_BF16>(c, groups, s) : grad_dt<MOE_F32>(c, groups, s);
     if (e != hipSuccess) return e;
-    float* dgate = c.n.gate_per_token ? nullptr : c.dgate;
-    if (!c.dpost && !dgate && !c.dpre) return hipSuccess;
-    hipLaunchKernelGGL(norm_parts_kernel, dim3((c.H + 63) / 64, 3), dim3(1024), 0, s, c.part, groups, c.H, c.dpost, dgate,
-                       c.dpre);
+    const bool block = c.dpost || (c.dgate && !c.n.gate_per_token);
+    if (!block && !c.dpre) return hipSuccess;
+    hipLaunchKernelGGL(norm_parts_kernel, dim3((c.H + 63) / 64, 2), dim3(1024), 0, s, c, groups);
     return hipGetLastError();
 }
 

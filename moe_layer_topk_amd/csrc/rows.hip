@@ -43,11 +43,11 @@ struct Piece {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// What rows are read and written beyond this many bytes goes past the caches
-// (non-temporal stores): permute of 16384 x 8 rows of 8 KB 246 -> 218 us, gradient of
-// 4096 x 8 of 4 KB 57 -> 47; below, rows just written are found there again (permute of
-// 4096 x 8 of 4 KB 26 us, non-temporal 28.5).
-constexpr int64_t kCacheBytes = 256ll << 20;
+// Beyond this many bytes read and written the rows go past the caches (non-temporal
+// stores).  Inputs changing from call to call: permute of 4096 x 8 rows of 4 KB 33.5 ->
+// 30.5 us, gradient of 4096 x 2 of 8 KB 40.3 -> 37.8; the same inputs again: permute of
+// 16384 x 8 of 8 KB 246 -> 218, of 4096 x 8 of 4 KB 26 -> 28.5 (its rows were still cached).
+constexpr int64_t kCacheBytes = 96ll << 20;
 
 // Zeroes the padding rows among rows [r0, r0 + 64) of the sorted list: a row
 // inside an expert's run (before the padded total) that holds no pair.

@@ -149,7 +149,7 @@ moe_status moe_residual_norm(moe_dtype dtype, const void* h, const void* y, cons
 
 size_t moe_residual_norm_workspace_size(int32_t M, int32_t H) {
     if (M <= 0 || H < 1) return 0;
-    return (size_t)norm_grad_groups(M, H) * 3 * H * sizeof(float);
+    return (size_t)norm_grad_groups(M, H) * 2 * H * sizeof(float);
 }
 
 moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const void* dh_out, const void* dx,
