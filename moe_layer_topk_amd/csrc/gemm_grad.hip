@@ -70,7 +70,21 @@ __device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
 // of 4096 x 14336, 8192 rows: 1480 -> 1285 us against 64 terms and one workgroup).  kZ
 // takes 64: its weight rows are read 128 bytes at a time, whole lines, instead of 64
 // (128 experts of 1536 x 2048, 16392 rows: 235 us against 270).
-enum DxMode { kDx, kDxSilu, kZ };
+enum DxMode { kDx, kDxSilu, kDxSiluNt, kZ };
+
+// 16 bytes of a row, NT: past the caches.
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const void* p) {
+    if constexpr (NT) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const u32x4*>(p)));
+    return *static_cast<const uint4*>(p);
+}
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+    if constexpr (NT)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), static_cast<u32x4*>(p));
+    else
+        *static_cast<uint4*>(p) = v;
+}
 
 template <int BM, int NS_>
 struct DxCfg {
@@ -89,7 +103,7 @@ template <int BM, int MODE, bool NTW, int NS>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NS == 32 ? 2 : 1, 2)))
 grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
     using C = DxCfg<BM, NS>;
-    constexpr bool SILU = MODE == kDxSilu;
+    constexpr bool SILU = MODE == kDxSilu || MODE == kDxSiluNt;
     extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
     // the row tiles that exist, cut into one range for each XCD (of those the grid allows
     // for, a batch of few rows an expert leaves a third or more empty, at the end)
@@ -261,7 +275,7 @@ grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
                 p[q] = (size_t)ids_s[r0 + min(r, rows - 1)];
                 if (SILU && col < O) {
                     const uint16_t* z = static_cast<const uint16_t*>(g.z) + p[q] * 2 * O + col;
-                    zg[q] = *reinterpret_cast<const uint4*>(z), zu[q] = *reinterpret_cast<const uint4*>(z + O);
+                    zg[q] = load16<MODE == kDxSiluNt>(z), zu[q] = load16<MODE == kDxSiluNt>(z + O);
                 }
             }
 #pragma unroll
@@ -298,11 +312,11 @@ grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
                         dg[x] = d[x] * uv * s * (1.0f + gv * (1.0f - s));
                     }
                     uint16_t* o = static_cast<uint16_t*>(g.out) + p[q] * 2 * O + col;
-                    *reinterpret_cast<uint4*>(o) = uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])};
-                    *reinterpret_cast<uint4*>(o + O) = uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])};
+                    store16<MODE == kDxSiluNt>(o, uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])});
+                    store16<MODE == kDxSiluNt>(o + O, uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])});
                     if (g.act)
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.act) + p[q] * O + col) =
-                            uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])};
+                        store16<MODE == kDxSiluNt>(static_cast<uint16_t*>(g.act) + p[q] * O + col,
+                                                   uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])});
                 } else {
                     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p[q] * O + col) = *reinterpret_cast<const uint4*>(at);
                 }
@@ -343,7 +357,11 @@ static hipError_t launch_dx_m(const GradCall& c, hipStream_t s) {
     return c.block_m == 128 ? launch_dx_w<128, MODE>(c, s) : launch_dx_w<64, MODE>(c, s);
 }
 
+// Past 96 MB of z, its gradients and activations they go past the caches (128 experts of
+// 2048 x 768, 16384 rows, 126 MB: 165 -> 148 us; 8 of 4096 x 14336, 8192 rows: 1145 ->
+// 1119; at 4096 rows of 128 experts, 31 MB, a tie).
 hipError_t launch_grad_dx(const GradCall& c, hipStream_t s) {
+    if (c.z && (int64_t)c.M * c.topk * c.K * 10 > (96ll << 20)) return launch_dx_m<kDxSiluNt>(c, s);
     return c.z ? launch_dx_m<kDxSilu>(c, s) : launch_dx_m<kDx>(c, s);
 }
 

@@ -133,6 +133,28 @@ def test_dx_through_silu(dev, M, k, E, H, I, block_m, how):
     close(act, wact, bact, "act")
 
 
+@pytest.mark.parametrize("block_m", [64, 128])
+def test_dx_through_silu_of_many_rows(dev, block_m):
+    """Over 96 MB of z, gradients and activations: they pass the caches."""
+    import moe_layer_topk_amd as moe
+    M, k, E, H, I = 4001, 2, 5, 128, 1408
+    ids, pairs, al, g = setup(dev, M, k, E, H, I, block_m, "dropped", 9)
+    dy, w, z = randn(g, M * k, H), randn(g, E, H, I, size=0.05), randn(g, M * k, 2 * I, size=3.0)
+    da, act = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_DOWN, dy.to(dev), w.to(dev), al, M, k, z=z.to(dev),
+                                      da=torch.full((M * k, 2 * I), 7.0, dtype=BF, device=dev),
+                                      act=torch.full((M * k, I), 7.0, dtype=BF, device=dev))
+    for e, p in enumerate(pairs):
+        p = p[::37]
+        a, b = dy[p].double(), w[e].double()
+        d, e_d = a @ b, 2 * H * U * (a.abs() @ b.abs())
+        want, wact, slope, mag = silu_grad(d, z[p].double())
+        close(da[p.to(dev)], want, HALF[BF] * want.abs() + torch.cat([e_d, e_d], 1) * slope * 1.01 + 16 * U * mag + 1e-38, "dz")
+        close(act[p.to(dev)], wact, (HALF[BF] + 16 * U) * wact.abs() + 1e-38, "act")
+    lost = torch.ones(M * k, dtype=torch.bool)
+    lost[torch.cat(pairs)] = False
+    assert (da[lost.to(dev)] == 7.0).all() and (act[lost.to(dev)] == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M,k,E,H,I,block_m,how", CASES + [(5000, 1, 1, 128, 128, 16, "one"), (4097, 2, 2, 128, 384, 1, "spread"),
                                                            (40, 2, 9, 256, 128, 256, "one")])

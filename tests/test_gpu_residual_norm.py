@@ -38,7 +38,12 @@ CASES = [(1, 8, F32, F32, True, True, "channel", True),
          (4, 16384, F32, F32, True, True, "token", True),
          (4, 16376, BF, BF, True, True, "channel", False),
          (1300, 264, BF, BF, True, True, "channel", True),
-         (700, 512, F32, F32, True, False, "token", True)]
+         (700, 512, F32, F32, True, False, "token", True),
+         (300, 1024, F32, F32, True, True, "channel", True),
+         (521, 512, BF, F32, True, False, "channel", True),
+         (257, 4096, F32, BF, True, True, "none", True),
+         (600, 4096, BF, BF, True, True, "channel", True),
+         (3, 12288, BF, F32, True, True, "token", True)]
 
 
 def make(M, H, dtype, wdtype, block, post, gate, pre, seed):

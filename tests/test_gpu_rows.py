@@ -70,6 +70,38 @@ def test_permute(dev, M, k, E, H, block_m, dtype, weighted, dropped):
         close(got, want, want.abs() * (HALF[dtype] * 1.01 + U), "rows")
 
 
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("M,k,E,H,block_m,dtype", [(3000, 4, 16, 4096, 128, BF), (1500, 4, 16, 4104, 64, F32)])
+def test_many_rows(dev, M, k, E, H, block_m, dtype, weighted):
+    """Over 96 MB of rows, which go by tokens: padding, dropped pairs and rows behind
+    the last run, and the gradients back."""
+    import moe_layer_topk_amd as moe
+    ids, x, w, g = make(M, k, E, H, dtype, weighted, True, 11)
+    al = moe.moe_align(ids.to(dev), E, block_m)
+    at = ref.pair_rows(ids, E, block_m)
+    s, off, _ = ref.align(ids, E, block_m)
+    assert len(s) * H * x.element_size() > 96 << 20
+    rows = torch.full((len(s), H), 7.0, dtype=dtype, device=dev)
+    wd = None if w is None else w.to(dev)
+    _, got_at = moe.moe_permute(x.to(dev), ids.to(dev), al, weights=wd, rows=rows)
+    assert torch.equal(got_at.cpu(), at)
+    live = at.view(-1) >= 0
+    held, owner = at.view(-1)[live].long(), torch.arange(M).repeat_interleave(k)[live]
+    want = torch.full((len(s), H), 7.0, dtype=torch.float64)
+    want[:off[E]] = 0.0
+    want[held] = x.double()[owner] * (1.0 if w is None else w.double().view(-1)[live][:, None])
+    close(rows, want, want.abs() * (HALF[dtype] * 1.01 + U) * (w is not None), "rows")
+    src = torch.randn(len(s), H, generator=g).to(dtype)
+    drows = torch.full_like(rows, 7.0)
+    _, dw = moe.moe_unpermute_backward(x.to(dev), None if w is None else src.to(dev), wd, at.to(dev), al, drows=drows)
+    assert torch.equal(drows, rows)  # the same product, w x
+    if w is not None:
+        prod = src.double()[held] * x.double()[owner]
+        wdw, mag = torch.zeros(M * k, dtype=torch.float64), torch.zeros(M * k, dtype=torch.float64)
+        wdw[live], mag[live] = prod.sum(1), prod.abs().sum(1)
+        close(dw.view(-1), wdw, (H + 2) * U * mag, "dweights")
+
+
 @pytest.mark.parametrize("dropped", [False, True])
 @pytest.mark.parametrize("M,k,E,H,block_m,dtype,weighted", CASES)
 def test_unpermute(dev, M, k, E, H, block_m, dtype, weighted, dropped):
