@@ -389,6 +389,7 @@ size_t fused_moe_noalloc_scratch_bytes(void);
  * contiguous, for programs that send them elsewhere or multiply them
  * themselves.  moe_grouped_gemm needs no such rows: it reads tokens and writes
  * pair order (row p of pair p), which the calls below take as pair_row NULL.
+ * Outputs lie apart from the inputs except where a call names one.
  *
  * moe_permute: token rows to expert order, with a weight each if given.
  *   rows[r] = w_p * x[p / topk] for every r that holds a pair p; the padding rows
@@ -421,6 +422,7 @@ moe_status moe_unpermute(moe_dtype dtype, const void* rows, int64_t nrows, const
  *   drows[r] = w_p * dout[p / topk],  dweights[p] = <rows[r], dout[p / topk]>, r = pair_row[p]
  * (float32 sums; dweights 0 for a pair with no row).  drows may be rows.
  *  dout      device [M][H], rows and drows [nrows][H], all in dtype
+ *  pair_row  no row twice (two pairs would write it)
  *  weights   NULL: 1 (then dweights must be NULL)
  *  rows, dweights   NULL together: no gradient of the weights
  *  al        non-NULL (needs pair_row): the padding rows of the experts' runs

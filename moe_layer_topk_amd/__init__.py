@@ -234,6 +234,8 @@ def moe_grouped_gemm(kind: int, a: torch.Tensor, w: torch.Tensor, al: dict, M: i
     if dt == MOE_FP8_BLOCK:
         return _block_gemm(kind, a, w, al, M, topk, a_scale, w_scale, c, c_amax)
     if kind == MOE_GEMM_GATE_UP:
+        if any(t is not None for t in (a_scale, w_scale, c_amax)):
+            raise ValueError("MOE_GEMM_GATE_UP is a bfloat16 product: it has no scales")
         return _gate_up_gemm(a, w, al, M, topk, c), None
     if dt == MOE_W4A16:
         K *= 2  # two 4-bit codes per byte

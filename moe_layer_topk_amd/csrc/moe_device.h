@@ -4,8 +4,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 namespace moe {
 
 constexpr int kWave = 64;
@@ -71,21 +69,6 @@ __device__ __forceinline__ unsigned wave_max_u32(unsigned x) {
     x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false));  // row_bcast:15
     x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false));  // row_bcast:31
     return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
-}
-
-// Sum of x over the wavefront, in every lane, in a fixed order: the moves of
-// wave_max_u32.
-__device__ __forceinline__ float wave_sum_f32(float x) {
-    auto move = [](float v, auto ctrl, auto rows) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
-    };
-    x += move(x, std::integral_constant<int, 0xB1>{}, std::integral_constant<int, 0xF>{});
-    x += move(x, std::integral_constant<int, 0x4E>{}, std::integral_constant<int, 0xF>{});
-    x += move(x, std::integral_constant<int, 0x141>{}, std::integral_constant<int, 0xF>{});
-    x += move(x, std::integral_constant<int, 0x140>{}, std::integral_constant<int, 0xF>{});
-    x += move(x, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
-    x += move(x, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
 // Routes token `t` with the calling wavefront; lane j < topk ends up holding

@@ -6,9 +6,26 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe.h"
 
 namespace moe {
+
+// Sum of x over the wavefront, in every lane, in a fixed order: the lane moves of
+// wave_max_u32 (no LDS).
+__device__ __forceinline__ float wave_sum_f32(float x) {
+    auto move = [](float v, auto ctrl, auto rows) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+    };
+    x += move(x, std::integral_constant<int, 0xB1>{}, std::integral_constant<int, 0xF>{});
+    x += move(x, std::integral_constant<int, 0x4E>{}, std::integral_constant<int, 0xF>{});
+    x += move(x, std::integral_constant<int, 0x141>{}, std::integral_constant<int, 0xF>{});
+    x += move(x, std::integral_constant<int, 0x140>{}, std::integral_constant<int, 0xF>{});
+    x += move(x, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+    x += move(x, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
 
 // Rows of tokens in expert order.  weights NULL: 1.  rows_in non-null: also
 // dots[p] = <rows_in[row of p], src[p / topk]>.  pair_row NULL: the row of pair p
