@@ -72,6 +72,10 @@ __device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
 // (128 experts of 1536 x 2048, 16392 rows: 235 us against 270).
 enum DxMode { kDx, kDxSilu, kDxSiluNt, kZ };
 
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return uint4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])};
+}
+
 // 16 bytes of a row, NT: past the caches.
 template <bool NT>
 __device__ __forceinline__ uint4 load16(const void* p) {
@@ -312,11 +316,10 @@ grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
                         dg[x] = d[x] * uv * s * (1.0f + gv * (1.0f - s));
                     }
                     uint16_t* o = static_cast<uint16_t*>(g.out) + p[q] * 2 * O + col;
-                    store16<MODE == kDxSiluNt>(o, uint4{pack_bf2(dg[0], dg[1]), pack_bf2(dg[2], dg[3]), pack_bf2(dg[4], dg[5]), pack_bf2(dg[6], dg[7])});
-                    store16<MODE == kDxSiluNt>(o + O, uint4{pack_bf2(du[0], du[1]), pack_bf2(du[2], du[3]), pack_bf2(du[4], du[5]), pack_bf2(du[6], du[7])});
+                    store16<MODE == kDxSiluNt>(o, pack8(dg));
+                    store16<MODE == kDxSiluNt>(o + O, pack8(du));
                     if (g.act)
-                        store16<MODE == kDxSiluNt>(static_cast<uint16_t*>(g.act) + p[q] * O + col,
-                                                   uint4{pack_bf2(ac[0], ac[1]), pack_bf2(ac[2], ac[3]), pack_bf2(ac[4], ac[5]), pack_bf2(ac[6], ac[7])});
+                        store16<MODE == kDxSiluNt>(static_cast<uint16_t*>(g.act) + p[q] * O + col, pack8(ac));
                 } else {
                     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + p[q] * O + col) = *reinterpret_cast<const uint4*>(at);
                 }
