@@ -67,9 +67,15 @@ __device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
 //
 // The gradients take 32 terms a stage, so that two workgroups fit a CU: one multiplies
 // while the other starts, waits at a barrier or writes out (down product of 8 experts
-// of 4096 x 14336, 8192 rows: 1480 -> 1285 us against 64 terms and one workgroup).  kZ
-// takes 64: its weight rows are read 128 bytes at a time, whole lines, instead of 64
-// (128 experts of 1536 x 2048, 16392 rows: 235 us against 270).
+// of 4096 x 14336, 8192 rows, through SiLU-and-mul: 1100 us against 1285 with 64 terms
+// and one workgroup; 128 experts of 1536 x 2048 at 16 rows 83 and 84).  kZ takes 64: its
+// weight rows are read 128 bytes at a time, whole lines, instead of 64 (128 experts of
+// 1536 x 2048, 16392 rows: 210 us against 233).
+//
+// What bounds them: at many rows an expert the power that products, transposing reads
+// and copies draw together (dx above: 0.87 PFLOP/s, matrix cores 50% busy at 1.4-1.5 GHz,
+// loads in flight 91% of the time; 740 us without copies and epilogue); at 128 rows the
+// way from L2 to LDS (8.7 TB/s); at 16 rows HBM (518 MB, 6.4 TB/s).
 enum DxMode { kDx, kDxSilu, kDxSiluNt, kZ };
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {

@@ -396,7 +396,8 @@ hipError_t launch_residual_norm(const NormCall& c, hipStream_t s) {
 }
 
 // Workgroups of the gradient kernel: two of 512 threads a CU, as many threads of
-// smaller ones (at 4096 x 4096 512 45 us, 256 49, 768 53), but eight rows each where
+// smaller ones (at 4096 x 4096, with a third column sum, 512 groups 45 us, 256 49, 768
+// 53; now 40), but eight rows each where
 // there are rows enough, since every group leaves 8 bytes a column to be added.
 int norm_grad_groups(int M, int H) {
     const int most = H > 2048 ? 512 : 1024;
@@ -429,8 +430,8 @@ static hipError_t grad_dt(const NormGrad& c, int groups, hipStream_t s) {
     if (c.H <= 512 * E) return grad_tv<DT, 512, 1, 4, true>(c, groups, s);
     if (c.H <= 1024 * E) return grad_tv<DT, 1024, 1, 4, true>(c, groups, s);
     // longer rows: pieces in a line, half as many wavefronts with all of the
-    // registers (16384 columns, 1024 rows: bfloat16 102 us, on 1024 threads 147 with
-    // registers spilled; float32 188 and 210)
+    // registers (16384 columns, 1024 rows: bfloat16 68 us, float32 147; with a third
+    // column sum 102 and 188, on 1024 threads, which spill registers, 147 and 210)
     if (DT == MOE_F32 && c.H <= 2048 * E) return grad_tv<DT, 512, 4, 2, false>(c, groups, s);
     return grad_tv<DT, 512, DT == MOE_F32 ? 8 : 4, 2, false>(c, groups, s);
 }

@@ -238,3 +238,11 @@ def test_binding_refusals():
                  lambda: moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP, b, torch.zeros(1, 256, 128, dtype=torch.bfloat16), {}, 4, 1)):
         with pytest.raises(ValueError, match="GPU only"):
             call()
+
+
+def test_gate_up_has_no_scales():
+    import moe_layer_topk_amd as moe
+    b, w, s = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(1, 256, 128, dtype=torch.bfloat16), torch.ones(1)
+    for more in (dict(a_scale=s), dict(w_scale=s), dict(c_amax=s)):
+        with pytest.raises(ValueError, match="scale"):
+            moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP, b, w, {}, 4, 1, **more)
