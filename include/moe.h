@@ -495,7 +495,9 @@ moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const 
  *         z [P][2K] (MOE_GEMM_GATE_UP's): the gradient goes on through
  *         SiLU-and-mul in float32 and da = dz [P][2K], gate columns first; act
  *         non-NULL then receives silu(gate) * up [P][K] of the same z.
- * Only rows of pairs with an expert are written.  al, block_m (64 or 128): as
+ * Only rows of pairs with an expert are written (moe_permute_backward over such
+ * pair rows needs a pair_row of -1 at the other pairs, or zeros in their rows).
+ * al, block_m (64 or 128): as
  * for moe_grouped_gemm.  Errors as there; one expert's weights of 4 GiB less
  * 64 KiB or more -> MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_gemm_dx(moe_gemm_kind kind, moe_dtype dtype, const void* dc, const void* w, const void* z,
