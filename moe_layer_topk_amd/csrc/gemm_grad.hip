@@ -96,6 +96,23 @@ __device__ __forceinline__ void store16(void* p, uint4 v) {
         *static_cast<uint4*>(p) = v;
 }
 
+// Eight columns through SiLU-and-mul's gradient: d the gradient of act, zg and zu the
+// products; dg, du their gradients, ac act.
+__device__ __forceinline__ void silu_grad8(const float (&d)[8], uint4 zg, uint4 zu, float (&dg)[8], float (&du)[8],
+                                           float (&ac)[8]) {
+    const uint32_t ug[4] = {zg.x, zg.y, zg.z, zg.w}, uu[4] = {zu.x, zu.y, zu.z, zu.w};
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const float gv = __uint_as_float((x & 1) ? ug[x / 2] & 0xffff0000u : ug[x / 2] << 16);
+        const float uv = __uint_as_float((x & 1) ? uu[x / 2] & 0xffff0000u : uu[x / 2] << 16);
+        const float s = 1.0f / (1.0f + __expf(-gv));
+        const float gs = gv * s;
+        du[x] = d[x] * gs;
+        ac[x] = gs * uv;
+        dg[x] = d[x] * uv * s * (1.0f + gv * (1.0f - s));
+    }
+}
+
 template <int BM, int NS_>
 struct DxCfg {
     static constexpr int ST = 3, Threads = 256, NS = NS_;  // NS: terms of the sum a stage
@@ -309,18 +326,8 @@ grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
                 if constexpr (SILU) {
                     const float4 d0 = *reinterpret_cast<const float4*>(at), d1 = *reinterpret_cast<const float4*>(at + 16);
                     const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-                    const uint32_t ug[4] = {zg[q].x, zg[q].y, zg[q].z, zg[q].w}, uu[4] = {zu[q].x, zu[q].y, zu[q].z, zu[q].w};
                     float dg[8], du[8], ac[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float gv = __uint_as_float((x & 1) ? ug[x / 2] & 0xffff0000u : ug[x / 2] << 16);
-                        const float uv = __uint_as_float((x & 1) ? uu[x / 2] & 0xffff0000u : uu[x / 2] << 16);
-                        const float s = 1.0f / (1.0f + __expf(-gv));
-                        const float gs = gv * s;
-                        du[x] = d[x] * gs;
-                        ac[x] = gs * uv;
-                        dg[x] = d[x] * uv * s * (1.0f + gv * (1.0f - s));
-                    }
+                    silu_grad8(d, zg[q], zu[q], dg, du, ac);
                     uint16_t* o = static_cast<uint16_t*>(g.out) + p[q] * 2 * O + col;
                     store16<MODE == kDxSiluNt>(o, pack8(dg));
                     store16<MODE == kDxSiluNt>(o + O, pack8(du));
@@ -351,6 +358,177 @@ static hipError_t launch_dx_t(const GradCall& c, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The same products where few workgroups would run: 64 rows x 128 columns a workgroup,
+// and of each stage of 128 terms a quarter for each of four groups of four wavefronts
+// (2 x 2 of 32 x 64), which have their own part of the ring; their sums are joined
+// through LDS, in order.  The time of a stage is its copies' way (0.5 us), whatever their
+// size: what helps are fewer stages and more workgroups.  Times below, at dx_few.
+struct SplitCfg {
+    static constexpr int BM = 64, BN = 128, G = 4, NS = 32, ST = 3, Threads = 256 * G;
+    static constexpr int ABytes = BM * NS * 2, WBytes = BN * NS * 2, PartBytes = ABytes + WBytes, StageBytes = G * PartBytes;
+    static constexpr int L = 3;                                  // copies a wave and stage
+    static constexpr int kRow = BN * 4 + 16, JoinBytes = BM * kRow;  // a group's sums
+    static constexpr int IdsOffset = ST * StageBytes, LdsBytes = IdsOffset + BM * 4;
+    static_assert(G * JoinBytes <= IdsOffset, "sums");
+    __device__ static __forceinline__ int swz(int c, int r) { return c ^ ((r / 4) % 4); }
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(SplitCfg::Threads) grad_dx_split_kernel(GradCall g, int o_tiles) {
+    using C = SplitCfg;
+    extern __shared__ __attribute__((aligned(1024))) char grad_lds[];
+    // (64-row parts of the list, whatever its block_m)
+    const int units = g.al.expert_offsets[g.E] / C::BM, nb = units * o_tiles, per = (nb + kXcds - 1) / kXcds;
+    const int l = blockIdx.x / kXcds, t = (blockIdx.x % kXcds) * per + l;
+    if (l >= per || t >= nb) return;
+    const int unit = t / o_tiles, o0 = (t % o_tiles) * C::BN;
+    const int e = g.al.tile_expert[unit * C::BM / g.block_m];
+    if (e < 0) return;
+    const int nreal = min(C::BM, g.al.expert_offsets[e] + g.al.expert_counts[e] - unit * C::BM);
+    if (nreal <= 0) return;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int grp = wave >> 2, wv = wave & 3, wm = wv >> 1, wn = wv & 1;
+    const int N = g.N, K = g.K, P = g.M * g.topk;
+    const int S = MODE == kZ ? K : N, O = MODE == kZ ? N : K;
+    const int32_t* sorted = g.al.sorted_ids + (size_t)unit * C::BM;
+    int* ids_s = reinterpret_cast<int*>(grad_lds + C::IdsOffset);
+    if (tid < C::BM) ids_s[tid] = sorted[tid];
+
+    // one copy of 16 rows of dc (kZ: of x) and two of W a wavefront and stage
+    const int ar = wv * 16 + (lane >> 2);
+    int ap = sorted[ar];
+    if ((unsigned)ap >= (unsigned)P) ap = sorted[0];
+    if (MODE == kZ) ap /= g.topk;
+    const char* asrc = static_cast<const char*>(g.dc) + (size_t)ap * S * 2 + grp * (C::NS * 2) + C::swz(lane & 3, ar) * 16;
+    const v4i_rsrc wrsrc = buf_rsrc(static_cast<const char*>(g.w) + (size_t)e * N * K * 2, (unsigned)((size_t)N * K * 2));
+    unsigned wsrc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (MODE == kZ) {
+            const int r = (wv * 2 + j) * 16 + (lane >> 2);
+            wsrc[j] = (unsigned)((size_t)(o0 + r) * K * 2) + grp * (C::NS * 2) + C::swz(lane & 3, r) * 16;
+        } else {
+            const int r = (wv * 2 + j) * 4 + (lane >> 4), c = lane & 15;
+            wsrc[j] = (unsigned)(((size_t)(grp * C::NS + r) * K + o0) * 2) + (tr_place(c >> 1, r) * 2 + (c & 1)) * 16;
+        }
+    }
+    const unsigned astep = C::G * C::NS * 2, wstep = MODE == kZ ? astep : astep * (unsigned)K;
+    const unsigned lds0 = lds_addr_of(grad_lds) + grp * C::PartBytes;
+    auto issue = [&](int kt) {
+        const unsigned st = lds0 + (unsigned)((kt % C::ST) * C::StageBytes);
+        lds_dma16_at(asrc + (size_t)kt * astep, st + wv * 1024);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) lds_dma16_buf(wrsrc, wsrc[j], kt * wstep, st + C::ABytes + (wv * 2 + j) * 1024);
+    };
+
+    f32x16 acc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[j][v] = 0.0f;
+    const int arow = wm * 32 + (lane & 31);
+    unsigned wlane[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        wlane[j] = C::ABytes + (MODE == kZ ? (wn * 64 + 32 * j + (lane & 31)) * (C::NS * 2) : tr_lane<C::BN>(lane, wn * 64 + 32 * j));
+    const bool live = nreal > wm * 32;
+
+    const int nk = S / (C::G * C::NS);
+#pragma unroll
+    for (int s0 = 0; s0 < C::ST - 1; ++s0)
+        if (s0 < nk) issue(s0);
+    for (int kt = 0; kt < nk; ++kt) {
+        if (kt + C::ST - 1 < nk)
+            wait_vm<(C::ST - 2) * C::L>();
+        else
+            wait_vm_runtime<C::L>(min(C::ST - 2, nk - 1 - kt));
+        __syncthreads();
+        if (kt + C::ST - 1 < nk) issue(kt + C::ST - 1);
+        if (live) {
+            const unsigned off = (unsigned)((kt % C::ST) * C::StageBytes);
+            const char* sa = grad_lds + grp * C::PartBytes + off;
+#pragma unroll
+            for (int ks = 0; ks < C::NS / 16; ++ks) {
+                const int c = ks * 2 + (lane >> 5);
+                const bf16x8 af = *reinterpret_cast<const bf16x8*>(sa + arow * (C::NS * 2) + (C::swz(c, arow) << 4));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    bf16x8 wf;
+                    if constexpr (MODE == kZ)
+                        wf = *reinterpret_cast<const bf16x8*>(sa + wlane[j] + (C::swz(c, lane & 31) << 4));
+                    else
+                        wf = tr_read8<C::BN>(lds0 + off + wlane[j] + ks * 16 * (2 * C::BN));
+                    acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf, af, acc[j], 0, 0, 0);
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<float4*>(grad_lds + grp * C::JoinBytes + arow * C::kRow +
+                                       (wn * 64 + 32 * j + 8 * v + 4 * (lane >> 5)) * 4) =
+                make_float4(acc[j][4 * v], acc[j][4 * v + 1], acc[j][4 * v + 2], acc[j][4 * v + 3]);
+    __syncthreads();
+    const int r = tid >> 4, c8 = (tid & 15) * 8;  // eight columns a thread
+    if (r >= nreal) return;
+    const size_t p = (size_t)ids_s[r];
+    float d[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const char* at = grad_lds + r * C::kRow + (c8 + 4 * h) * 4;
+        float4 sum = *reinterpret_cast<const float4*>(at);
+#pragma unroll
+        for (int q = 1; q < C::G; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(at + q * C::JoinBytes);
+            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+        }
+        d[4 * h] = sum.x, d[4 * h + 1] = sum.y, d[4 * h + 2] = sum.z, d[4 * h + 3] = sum.w;
+    }
+    const int col = o0 + c8;
+    uint16_t* out = static_cast<uint16_t*>(g.out);
+    if constexpr (MODE == kDxSilu) {
+        const uint16_t* z = static_cast<const uint16_t*>(g.z) + p * 2 * O + col;
+        float dg[8], du[8], ac[8];
+        silu_grad8(d, load16<false>(z), load16<false>(z + O), dg, du, ac);
+        uint16_t* o = out + p * 2 * O + col;
+        store16<false>(o, pack8(dg));
+        store16<false>(o + O, pack8(du));
+        if (g.act) store16<false>(static_cast<uint16_t*>(g.act) + p * O + col, pack8(ac));
+    } else {
+        store16<false>(out + p * O + col, pack8(d));
+    }
+}
+
+// Up to 300 workgroups of it (of a guess: every expert hit, the last part of each half
+// full).  Regular against split, us, with its workgroups: dx of 8 experts, 2112 rows, 11008
+// terms, 168: 147 and 64; 128 experts of 1536 x 2048, 8 rows, 128: 22 and 12; 4096 terms,
+// 288: 59 and 51; 1536 terms, 464: 29 and 32; through SiLU, 5888 terms, 39: 71 and 30;
+// 1024 terms, 576: 31 and 37; gate/up of 2560 terms, 32: 30 and 14; 2432 terms, 260: 34
+// and 21; 2048 terms, 348: 32 and 34; 1024 terms, 384: 18 and 23.
+static bool dx_few(const GradCall& c, int O) {
+    const int64_t P = (int64_t)c.M * c.topk, hit = P < c.E ? P : c.E, full = P / SplitCfg::BM + hit / 2;
+    return (hit > full ? hit : full) * (O / SplitCfg::BN) <= 300;
+}
+
+template <int MODE>
+static hipError_t launch_dx_split(const GradCall& c, hipStream_t s) {
+    using C = SplitCfg;
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad_dx_split_kernel<MODE>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::LdsBytes);
+    if (attr != hipSuccess) return attr;
+    const int o_tiles = (MODE == kZ ? c.N : c.K) / C::BN;
+    const int64_t nb = moe_align_capacity(c.M, c.topk, c.E, c.block_m) / C::BM * o_tiles;
+    hipLaunchKernelGGL((grad_dx_split_kernel<MODE>), dim3((unsigned)((nb + kXcds - 1) / kXcds * kXcds)), dim3(C::Threads),
+                       C::LdsBytes, s, c, o_tiles);
+    return hipGetLastError();
+}
+
 // Weights go past the caches (non-temporal) while an expert's rows mostly fit one row
 // tile: dx of 128 experts of 1536 x 2048 at 16 rows each 136 -> 123 us, at 96 167 -> 153,
 // at 128 203 against 224; gate/up of 8 of 28672 x 4096 at 16 320 -> 293, at 96 355 -> 333,
@@ -363,6 +541,7 @@ static hipError_t launch_dx_w(const GradCall& c, hipStream_t s) {
 
 template <int MODE>
 static hipError_t launch_dx_m(const GradCall& c, hipStream_t s) {
+    if (dx_few(c, MODE == kZ ? c.N : c.K)) return launch_dx_split<MODE == kDxSiluNt ? kDxSilu : MODE>(c, s);
     return c.block_m == 128 ? launch_dx_w<128, MODE>(c, s) : launch_dx_w<64, MODE>(c, s);
 }
 

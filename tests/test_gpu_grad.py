@@ -304,3 +304,27 @@ def test_repeat_streams_and_graphs(dev):
         x.copy_(randn(g, M, H).to(dev))
         got = run(graph.replay)
         assert all(torch.equal(a, b) for a, b in zip(got, run(step)))
+
+
+#       M    k  E    H     I    block_m how: sizes of many workgroups, for experts of few rows and of many
+MANY = [(120, 2, 160, 256, 256, 64, "spread"),
+        (121, 2, 160, 384, 384, 128, "dropped"),
+        (1030, 2, 20, 1152, 1152, 64, "spread"),
+        (1030, 2, 20, 1152, 1152, 128, "dropped"),
+        (1000, 2, 4, 1280, 1280, 128, "one")]
+
+
+@pytest.mark.parametrize("M,k,E,H,I,block_m,how", MANY)
+def test_products_of_many_workgroups(dev, M, k, E, H, I, block_m, how):
+    test_gate_up(dev, M, k, E, H, I, block_m, how)
+    test_dx_plain(dev, M, k, E, H, I, block_m, how)
+    test_dx_through_silu(dev, M, k, E, H, I, block_m, how)
+
+
+@pytest.mark.parametrize("M,k,E,H,I,block_m,how", [(3, 1, 2, 128, 2176, 64, "spread"),    # sums of one stage and of many
+                                                   (65, 1, 1, 2176, 128, 128, "one"),     # a part of one row, sums of 17
+                                                   (129, 1, 2, 1152, 256, 128, "one")])
+def test_products_of_few_workgroups(dev, M, k, E, H, I, block_m, how):
+    test_gate_up(dev, M, k, E, H, I, block_m, how)
+    test_dx_plain(dev, M, k, E, H, I, block_m, how)
+    test_dx_through_silu(dev, M, k, E, H, I, block_m, how)
