@@ -565,7 +565,8 @@ hipError_t launch_gate_up(const GradCall& c, hipStream_t s) { return launch_dx_m
 // B = 256: eight wavefronts, two a SIMD, a workgroup a CU; bound by the power that
 // products, LDS reads and copies draw together (the clock falls to 1.7 GHz).  B = 128:
 // four wavefronts and a third of the LDS, three workgroups a CU, so that one begins
-// while another is stored: for experts of few rows, whose results' stores are the work.
+// while another is stored: for experts of few rows, whose results' stores are the work, and
+// where few workgroups of the larger tile would run.
 
 template <int B>
 struct DwCfg {
@@ -747,7 +748,11 @@ static hipError_t launch_dw_o(const GradCall& c, hipStream_t s) {
     // 173 and 150 -> 140, at 512 rows 349 against 387 and 288 against 311; of 1536 x 2048
     // at 64 rows 279 -> 264 and 180 -> 169.  Matrices of 4096 x 14336 at 64 rows: float32
     // 353 against 386, bfloat16 212 and 202.
-    const bool small = (int64_t)c.N * c.K <= (8 << 20) && (int64_t)c.M * c.topk <= 192ll * c.E;
+    // Also where 256 x 256 tiles are up to 160 workgroups, with any rows: 4 of 512 x 512 at
+    // 1024 rows each 27 -> 16 us, 8 of 1024 x 1024 at 512 rows (128 workgroups) 19 -> 16, at
+    // 1024 rows 29 -> 28; of 2048 x 1024 at 1024 rows (256) 38 against 45.
+    const int64_t large = (int64_t)c.E * ((c.N + 255) / 256) * ((c.K + 255) / 256);
+    const bool small = large <= 160 || ((int64_t)c.N * c.K <= (8 << 20) && (int64_t)c.M * c.topk <= 192ll * c.E);
     return small ? launch_dw_t<ODT, 128>(c, s) : launch_dw_t<ODT, 256>(c, s);
 }
 

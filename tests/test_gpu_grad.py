@@ -328,3 +328,12 @@ def test_products_of_few_workgroups(dev, M, k, E, H, I, block_m, how):
     test_gate_up(dev, M, k, E, H, I, block_m, how)
     test_dx_plain(dev, M, k, E, H, I, block_m, how)
     test_dx_through_silu(dev, M, k, E, H, I, block_m, how)
+
+
+#  256 x 256 tiles, few workgroups' worth of them and more, with rows for several stages
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,k,E,H,I,block_m,how", [(2100, 2, 20, 640, 384, 64, "spread"), (1100, 2, 2, 2432, 1152, 128, "dropped"),
+                                                   (700, 1, 9, 1152, 1152, 128, "spread"), (1500, 3, 41, 512, 256, 64, "one"),
+                                                   (1401, 3, 21, 640, 384, 128, "dropped"), (1400, 3, 21, 384, 640, 1, "one")])
+def test_dw_of_more_rows(dev, M, k, E, H, I, block_m, how, dtype):
+    test_dw(dev, M, k, E, H, I, block_m, how, dtype)
