@@ -496,7 +496,8 @@ moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const 
  *         SiLU-and-mul in float32 and da = dz [P][2K], gate columns first; act
  *         non-NULL then receives silu(gate) * up [P][K] of the same z.
  * Only rows of pairs with an expert are written (moe_permute_backward over such
- * pair rows needs a pair_row of -1 at the other pairs, or zeros in their rows).
+ * pair rows needs a pair_row of -1 at the other pairs, or zeros in their rows;
+ * so do moe_unpermute, moe_combine and moe_unpermute_backward over y).
  * al, block_m (64 or 128): as
  * for moe_grouped_gemm.  Errors as there; one expert's weights of 4 GiB less
  * 64 KiB or more -> MOE_ERR_UNSUPPORTED. */

@@ -324,7 +324,9 @@ def moe_grouped_gemm_dx(kind: int, dc: torch.Tensor, w: torch.Tensor, al: dict, 
     kind MOE_GEMM_GATE_UP: dc = dz [P, 2I], w = w1, da [P, H].  MOE_GEMM_DOWN: dc =
     dy [P, H], w = w2, da [P, I], or with z (moe_grouped_gemm's GATE_UP) the
     gradient dz [P, 2I] before SiLU-and-mul, and act = silu(gate) * up [P, I].
-    Returns (da, act or None)."""
+    Rows of pairs whose id is no expert are not written, as in moe_grouped_gemm: an
+    allocated da has whatever was there (see moe_permute_backward).  Returns (da, act
+    or None)."""
     E, N, K = w.shape
     P, dev = M * topk, w.device
     stream = _stream(w)
@@ -437,7 +439,7 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, al: dict, weights=None,
 def moe_unpermute(rows: torch.Tensor, pair_row=None, weights=None, topk=None, out_dtype=None, out=None):
     """Expert rows back to token order: out[t] = sum_j w_tj rows[pair_row[t, j]]
     (weights None: 1; pairs without a row add nothing; pair_row None: rows in pair
-    order, with topk where no weights say it)."""
+    order, with topk where no weights say it, every one of which is added)."""
     dev = rows.device
     stream = _stream(rows)
     k, M, nrows, H = _rows_shape("rows", rows, pair_row, weights, topk)
@@ -456,7 +458,9 @@ def moe_unpermute_backward(dout: torch.Tensor, rows, weights, pair_row=None, al=
     drows[r] = w_p dout[p // k] and dweights [M, k], dweights[p] = <rows[r], dout[p // k]>.
     rows None: no gradient of the weights (then nrows says how many rows there are
     when neither pair order nor al does).  al: the alignment the rows follow; the
-    padding rows of its runs become zeros.  drows may be rows.  Returns (drows,
+    padding rows of its runs become zeros.  drows may be rows.  Pair order counts
+    every pair: with ids that are no expert it needs the pair_row of
+    moe_permute_backward, as rows of such pairs hold nothing.  Returns (drows,
     dweights or None)."""
     M, H = dout.shape
     dev = dout.device
@@ -509,7 +513,11 @@ def moe_unpermute_backward(dout: torch.Tensor, rows, weights, pair_row=None, al=
 def moe_permute_backward(drows: torch.Tensor, pair_row=None, x=None, weights=None, topk=None, dx=None, dweights=None):
     """Gradients of moe_permute for drows: dx[t] = sum_j w_tj drows[pair_row[t, j]], and
     with x (and weights) dweights[p] = <drows[r], x[p // k]>.  pair_row None: rows in
-    pair order (moe_grouped_gemm_dx).  Returns (dx, dweights or None)."""
+    pair order (moe_grouped_gemm_dx), every one of which is added.  The grouped products
+    leave the rows of pairs without an expert unwritten: with such ids [M, k] give
+    pair_row = torch.where((ids >= 0) & (ids < E), torch.arange(M * k, dtype=torch.int32,
+    device=ids.device).view(M, k), -1), here and in moe_unpermute (in place of
+    moe_combine) and moe_unpermute_backward.  Returns (dx, dweights or None)."""
     dev = drows.device
     stream = _stream(drows)
     k, M, nrows, H = _rows_shape("drows", drows, pair_row, weights, topk)

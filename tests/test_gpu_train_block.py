@@ -141,3 +141,69 @@ def test_block_in_a_graph(dev):
         eager = block(moe, p, M, E, k, H, I, 0.8, False)
         torch.cuda.synchronize()
         assert all(torch.equal(got[n], eager[n]) for n in got)
+
+
+@pytest.mark.parametrize("M,E,k,H,I", [(2, 3, 2, 128, 128), (75, 16, 4, 384, 256), (260, 4, 2, 512, 384)])
+def test_pairs_of_no_expert(dev, M, E, k, H, I):
+    """The products' forward and backward in pair order with ids that are no expert (a
+    whole token of them among them): with a pair_row of -1 there nothing of the rows that
+    the products leave unwritten, here NaN, gets into any result.
+
+    Bounds: a float32 sum of n terms is off by at most n U times the sum of their
+    magnitudes, 2 n U for the matrix instructions; results add their own rounding."""
+    import moe_layer_topk_amd as moe
+    from train_ref import HALF, U, close
+    p = {n: t.to(dev) for n, t in make(M, E, k, H, I, 11).items()}
+    g = torch.Generator().manual_seed(12)
+    P, F32 = M * k, torch.float32
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    ids = torch.where(torch.rand(M, k, generator=g) < 0.3, torch.where(torch.rand(M, k, generator=g) < 0.5, -1, E), ids).int()
+    ids[1], ids[0, 0] = -1, 0
+    ids, wts = ids.to(dev), torch.rand(M, k, generator=g).to(dev)
+    held = (ids >= 0) & (ids < E)
+    pair_row = torch.where(held, torch.arange(P, dtype=torch.int32, device=dev).view(M, k), -1)
+    assert pair_row.dtype == torch.int32
+    x, dout = (0.5 * p["h"].float()).to(BF), p["dout"]
+
+    def nan(cols):
+        return torch.full((P, cols), float("nan"), dtype=BF, device=dev)
+
+    al = moe.moe_align(ids, E, 64)
+    z, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP, x, p["w1"], al, M, k, c=nan(2 * I))
+    act, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP_SILU, x, p["w1"], al, M, k, c=nan(I))
+    y, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_DOWN, act, p["w2"], al, M, k, c=nan(H))
+    out = moe.moe_unpermute(y, pair_row, wts)
+    dy, dwts = moe.moe_unpermute_backward(dout, y, wts, pair_row, drows=nan(H))
+    dz, _ = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_DOWN, dy, p["w2"], al, M, k, z=z, da=nan(2 * I), act=nan(I))
+    dw2 = moe.moe_grouped_gemm_dw(moe.MOE_GEMM_DOWN, dy, act, al, M, k, dtype=F32)
+    dxp, _ = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_GATE_UP, dz, p["w1"], al, M, k, da=nan(H))
+    dw1 = moe.moe_grouped_gemm_dw(moe.MOE_GEMM_GATE_UP, dz, x, al, M, k, dtype=F32)
+    dx, none = moe.moe_permute_backward(dxp, pair_row)
+    assert none is None
+    lost = ~held.view(-1)
+    for t in (z, act, y, dy, dz, dxp):  # unwritten where no expert is, numbers elsewhere
+        assert torch.isnan(t[lost]).all() and torch.isfinite(t[~lost]).all()
+
+    at, live = pair_row.cpu(), held.cpu()
+    w = wts.cpu().double()
+    want, mag = ref.unpermute(y.cpu(), at, wts.cpu())
+    close(out, want, HALF[BF] * want.abs() + 2 * (k + 1) * U * mag, "out")
+    yk = torch.where(live[:, :, None], y.cpu().double().view(M, k, H), 0.0)
+    prod = yk * dout.cpu().double()[:, None, :]
+    close(dwts, prod.sum(2), (H + 2) * U * prod.abs().sum(2), "dweights")
+    want = (dout.cpu().double()[:, None, :] * w[:, :, None]).view(P, H)[live.view(-1)]
+    close(dy[~lost], want, want.abs() * (HALF[BF] * 1.01 + U), "dy")
+    want, mag = ref.unpermute(dxp.cpu(), at, None)
+    close(dx, want, HALF[BF] * want.abs() + 2 * (k + 1) * U * mag, "dx")
+    for t in (out, dx, dwts):
+        assert not t[1].any()  # the token with no expert at all
+    flat = ids.cpu().view(-1)
+    for e in range(E):
+        i = (flat == e).nonzero().flatten()
+        for got, d, a in ((dw2, dy.cpu()[i], act.cpu()[i]), (dw1, dz.cpu()[i], x.cpu()[i // k])):
+            d, a = d.double(), a.double()
+            want = d.t() @ a
+            close(got[e], want, HALF[F32] * want.abs() + 2 * max(len(i), 1) * U * (d.abs().t() @ a.abs()), f"dw expert {e}")
+    dxp[lost] = 0  # the other way: rows of zeros, every pair added
+    again, _ = moe.moe_permute_backward(dxp, topk=k)
+    assert torch.equal(again, dx)
