@@ -495,6 +495,8 @@ moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const 
  *         z [P][2K] (MOE_GEMM_GATE_UP's): the gradient goes on through
  *         SiLU-and-mul in float32 and da = dz [P][2K], gate columns first; act
  *         non-NULL then receives silu(gate) * up [P][K] of the same z.
+ *         (That act comes from z as stored; MOE_GEMM_GATE_UP_SILU's from z before
+ *         its rounding.  The gradient of a y made from the latter takes the latter.)
  * Only rows of pairs with an expert are written (moe_permute_backward over such
  * pair rows needs a pair_row of -1 at the other pairs, or zeros in their rows;
  * so do moe_unpermute, moe_combine and moe_unpermute_backward over y).

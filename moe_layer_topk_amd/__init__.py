@@ -323,7 +323,9 @@ def moe_grouped_gemm_dx(kind: int, dc: torch.Tensor, w: torch.Tensor, al: dict, 
     """Gradient of the rows of a grouped product (bfloat16): da[p] = w[e]^T dc[p].
     kind MOE_GEMM_GATE_UP: dc = dz [P, 2I], w = w1, da [P, H].  MOE_GEMM_DOWN: dc =
     dy [P, H], w = w2, da [P, I], or with z (moe_grouped_gemm's GATE_UP) the
-    gradient dz [P, 2I] before SiLU-and-mul, and act = silu(gate) * up [P, I].
+    gradient dz [P, 2I] before SiLU-and-mul, and act = silu(gate) * up [P, I] (of z as
+    stored: the act of MOE_GEMM_GATE_UP_SILU, from z before its rounding, is the one
+    whose product with dy is the gradient of the y it made).
     Rows of pairs whose id is no expert are not written, as in moe_grouped_gemm: an
     allocated da has whatever was there (see moe_permute_backward).  Returns (da, act
     or None)."""

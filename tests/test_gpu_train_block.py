@@ -207,3 +207,41 @@ def test_pairs_of_no_expert(dev, M, E, k, H, I):
     dxp[lost] = 0  # the other way: rows of zeros, every pair added
     again, _ = moe.moe_permute_backward(dxp, topk=k)
     assert torch.equal(again, dx)
+
+
+def test_dw2_is_the_gradient_of_the_y_that_was_made(dev):
+    """y = act W2 is linear in W2: over any direction V the differences of <y, dy> are
+    exactly <dW2, V> with dW2 = dy^T act of the act that y was made of, to the float32
+    sums of the pairs (2 n U of the magnitudes).  The act made again from z is another
+    one: off by the roundings of gate and up (silu's slope is at most 1.1), the sums of
+    the two products, and both acts' own roundings."""
+    import moe_layer_topk_amd as moe
+    from train_ref import HALF, U, close
+    M, E, k, H, I = 200, 4, 2, 256, 384
+    p = {n: t.to(dev) for n, t in make(M, E, k, H, I, 13).items()}
+    g = torch.Generator().manual_seed(14)
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32).to(dev)
+    x, dy = (0.5 * p["h"].float()).to(BF), torch.randn(M * k, H, generator=g).to(BF).to(dev)
+    al = moe.moe_align(ids, E, 64)
+    z, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP, x, p["w1"], al, M, k)
+    act, _ = moe.moe_grouped_gemm(moe.MOE_GEMM_GATE_UP_SILU, x, p["w1"], al, M, k)
+    kept = act.clone()
+    _, again = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_DOWN, dy, p["w2"], al, M, k, z=z)
+    assert torch.equal(act, kept)  # the forward's act is left alone
+    dw2 = moe.moe_grouped_gemm_dw(moe.MOE_GEMM_DOWN, dy, act, al, M, k, dtype=torch.float32)
+    flat = ids.view(-1).cpu()
+    v = torch.randn(E, H, I, generator=g, dtype=torch.float64)
+    for e in range(E):
+        i = (flat == e).nonzero().flatten()
+        d, a = dy.cpu()[i].double(), act.cpu()[i].double()
+        along = ((a @ v[e].t()) * d).sum()  # (y(W2 + s V) - y(W2)) / s against dy
+        assert abs(along - (dw2[e].cpu().double() * v[e]).sum()) <= 2 * len(i) * U * ((d.abs().t() @ a.abs()) * v[e].abs()).sum()
+    zd, e_z = z.cpu().double(), torch.zeros(M * k, 2 * I, dtype=torch.float64)
+    for e in range(E):
+        i = (flat == e).nonzero().flatten()
+        e_z[i] = 4 * H * U * (x.cpu()[i // k].double().abs() @ p["w1"][e].cpu().double().abs().t())  # (two products' sums)
+    size, off = zd.abs(), 1.01 * HALF[BF] * zd.abs() + e_z
+    gt, up, d_gt, d_up = size[:, :I], size[:, I:], off[:, :I], off[:, I:]
+    a, b = act.cpu().double(), again.cpu().double()
+    moved = 1.1 * d_gt * (up + d_up) + (gt + d_gt) * d_up  # (silu itself is at most its argument)
+    close(again, a, moved + (1.01 * HALF[BF] + 16 * U) * (a.abs() + b.abs()) + 1e-38, "act")
