@@ -327,3 +327,56 @@ def test_streams_and_graphs(dev):
         assert all(torch.equal(a, b) for a, b in zip(got, results()))
         if i == 0:
             assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+def test_differences_to_the_sums_roundings(dev):
+    """As above, from buffers that hold nothing but what was put there, each bound from
+    the magnitudes S that meet in it: an operand moved by v (1 U), its product (1 U), on
+    both sides; a sum over a token's k rows ((k + 1) U) or over a row's H terms
+    ((H + 2) U), on both sides of a difference or once, against 2 v."""
+    import moe_layer_topk_amd as moe
+    g = torch.Generator().manual_seed(16)
+    M, k, E, H, bm = 23, 4, 12, 264, 16
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32).to(dev)
+    al = moe.moe_align(ids, E, bm)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g).to(dev)
+
+    x, w, dout, vx, vw = randn(M, H), torch.rand(M, k, generator=g).to(dev), randn(M, H), randn(M, H), randn(M, k)
+    empty = torch.zeros(al["sorted_ids"].numel(), H, device=dev)
+    d, vr = randn(*empty.shape), randn(*empty.shape)
+    rows, at = moe.moe_permute(x, ids, al, weights=w, rows=empty.clone())
+    held = at.view(-1).long()
+
+    def pairs(t):  # [M, k, H] of expert rows
+        return t.double()[held].view(M, k, H)
+
+    def tok(t):  # [M, 1, H] of token rows
+        return t.double()[:, None, :]
+
+    def wgt(t):  # [M, k, 1] of weights
+        return t.double()[:, :, None]
+
+    def check(lhs, rhs, terms, mags, what):
+        bound = terms * U * float(mags.expand(M, k, H).sum())
+        assert abs(float(lhs) - float(rhs)) <= bound, f"{what}: {float(lhs)} and {float(rhs)}, bound {bound}"
+
+    def there(x, w):
+        r, _ = moe.moe_permute(x, ids, al, weights=w, rows=empty.clone())
+        return (r.double() * d.double()).sum()
+
+    dx, dwp = moe.moe_permute_backward(d, at, x, w)
+    check(there(x + vx, w) - there(x - vx, w), 2 * (vx.double() * dx.double()).sum(), 2 * k + 7,
+          wgt(w).abs() * (tok(x).abs() + tok(vx).abs()) * pairs(d).abs(), "dx")
+    check(there(x, w + vw) - there(x, w - vw), 2 * (vw.double() * dwp.double()).sum(), 2 * H + 9,
+          (wgt(w).abs() + wgt(vw).abs()) * tok(x).abs() * pairs(d).abs(), "dweights of permute")
+
+    def back(r, w):
+        return (moe.moe_unpermute(r, at, w).double() * dout.double()).sum()
+
+    drows, dwu = moe.moe_unpermute_backward(dout, rows, w, at, al, drows=empty.clone())
+    check(back(rows + vr, w) - back(rows - vr, w), 2 * (pairs(vr) * pairs(drows)).sum(), 2 * k + 7,
+          wgt(w).abs() * (pairs(rows).abs() + pairs(vr).abs()) * tok(dout).abs(), "drows")
+    check(back(rows, w + vw) - back(rows, w - vw), 2 * (vw.double() * dwu.double()).sum(), 2 * H + 2 * k + 9,
+          (wgt(w).abs() + wgt(vw).abs()) * pairs(rows).abs() * tok(dout).abs(), "dweights of unpermute")
