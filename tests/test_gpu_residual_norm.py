@@ -281,3 +281,60 @@ def test_graphs(dev):
         eager = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (*bufs, *eager[2:])))
+
+
+#  What the cases above leave out: every way a row is held (threads, pieces a thread, rows
+#  that fill their workgroup or not), each with more rows than workgroups, so that sums go
+#  on from row to row, the shared buffers alternate and the next row is on its way.
+#  (Long rows add 32 values in a thread, 6 times across a wavefront and 8 wavefronts: 46
+#  in a line, under the 64 above.)
+#        M    H     dtype wdtype block post  gate      pre
+MORE = [(300, 1000, BF, BF, True, True, "channel", True),      # 128 threads
+        (520, 1024, BF, F32, True, True, "none", True),
+        (1030, 1032, BF, BF, True, True, "token", True),       # 256
+        (600, 2040, BF, BF, True, True, "channel", True),
+        (520, 2048, BF, F32, True, False, "channel", True),
+        (600, 4088, BF, BF, True, True, "token", True),        # 512
+        (300, 4104, BF, BF, True, True, "channel", True),      # 1024
+        (600, 5120, BF, F32, True, True, "channel", True),
+        (520, 6144, BF, BF, True, True, "token", True),
+        (515, 7168, BF, BF, False, False, "none", True),
+        (600, 8184, BF, BF, True, False, "none", False),
+        (600, 8192, BF, BF, True, True, "channel", True),
+        (600, 8200, BF, BF, True, True, "token", True),        # long rows
+        (530, 12288, BF, F32, True, True, "channel", True),
+        (600, 16384, BF, BF, True, True, "channel", True),
+        (600, 248, F32, F32, True, True, "channel", True),     # 64
+        (300, 256, F32, BF, True, True, "none", True),
+        (520, 512, F32, F32, True, True, "channel", True),     # 128
+        (600, 1016, F32, F32, True, True, "token", True),      # 256
+        (520, 1032, F32, F32, True, True, "channel", True),    # 512
+        (600, 2040, F32, BF, True, True, "token", True),
+        (1100, 2048, F32, F32, True, True, "channel", True),
+        (600, 2056, F32, F32, True, True, "channel", True),    # 1024
+        (520, 4088, F32, BF, True, False, "token", True),
+        (600, 4096, F32, F32, True, True, "channel", True),
+        (600, 4104, F32, F32, True, True, "channel", True),    # long rows
+        (520, 8192, F32, BF, True, True, "token", True),
+        (520, 8200, F32, F32, True, True, "token", True),
+        (600, 16384, F32, F32, True, True, "channel", True)]
+
+
+@pytest.mark.parametrize("M,H,dtype,wdtype,block,post,gate,pre", MORE)
+def test_every_way_a_row_is_held(dev, M, H, dtype, wdtype, block, post, gate, pre):
+    test_forward(dev, M, H, dtype, wdtype, block, post, gate, pre)
+    test_backward(dev, M, H, dtype, wdtype, block, post, gate, pre)
+
+
+def test_long_rows_over_every_input(dev):
+    """Rows of several pieces a thread over each of their inputs: the same bits as apart."""
+    import moe_layer_topk_amd as moe
+    for H, dtype in ((12288, BF), (4104, F32), (16384, F32)):
+        c = make(560, H, dtype, dtype, True, True, "channel", True, 21)
+        kw = weights(c, dev)
+        names = ("h", "dh_out", "dx", "y")
+        apart = moe.moe_residual_norm_backward(*(c[k].to(dev) for k in names), **kw)
+        for over in ((0, 1), (1, 2), (2, 3), (3, 0)):
+            args = [c[k].to(dev) for k in names]
+            got = moe.moe_residual_norm_backward(*args, **kw, dh=args[over[0]], dy=args[over[1]])
+            assert all(torch.equal(a, b) for a, b in zip(apart, got)), (H, over)
