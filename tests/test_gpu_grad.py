@@ -337,3 +337,44 @@ def test_products_of_few_workgroups(dev, M, k, E, H, I, block_m, how):
                                                    (1401, 3, 21, 640, 384, 128, "dropped"), (1400, 3, 21, 384, 640, 1, "one")])
 def test_dw_of_more_rows(dev, M, k, E, H, I, block_m, how, dtype):
     test_dw(dev, M, k, E, H, I, block_m, how, dtype)
+
+
+def test_silu_gradient_past_four_gib(dev):
+    """z and its gradients of 70000 x 32768 (4.6 GB each): rows and columns from their far ends."""
+    import moe_layer_topk_amd as moe
+    M, H, I = 70000, 128, 16384
+    al = moe.moe_align(torch.zeros(M, 1, dtype=torch.int32, device=dev), 1, 128)
+    g = torch.Generator(device=dev).manual_seed(10)
+    z = torch.empty(M, 2 * I, dtype=BF, device=dev)
+    for i in range(0, M, 10000):
+        z[i:i + 10000] = torch.randn(10000, 2 * I, generator=g, device=dev).to(BF)
+    assert z.numel() * 2 > 2 ** 32
+    w = (torch.randn(1, H, I, generator=g, device=dev) * 0.05).to(BF)
+    dy = torch.randn(M, H, generator=g, device=dev).to(BF)
+    da, act = moe.moe_grouped_gemm_dx(moe.MOE_GEMM_DOWN, dy, w, al, M, 1, z=z)
+    for r in (slice(0, 3), slice(33333, 33336), slice(M - 3, M)):
+        a, b = dy[r].cpu().double(), w[0].cpu().double()
+        d, e_d = a @ b, 2 * H * U * (a.abs() @ b.abs())
+        want, wact, slope, mag = silu_grad(d, z[r].cpu().double())
+        close(da[r], want, HALF[BF] * want.abs() + torch.cat([e_d, e_d], 1) * slope * 1.01 + 16 * U * mag + 1e-38, "dz")
+        close(act[r], wact, (HALF[BF] + 16 * U) * wact.abs() + 1e-38, "act")
+
+
+def test_large_dw_tiles_past_four_gib(dev):
+    """dc of 70000 x 32768 (4.6 GB) against 384 columns: 256 tiles of 256 x 256, whose rows
+    and columns lie past 32 bits (test_operands_past_four_gib has few enough for the
+    smaller ones)."""
+    import moe_layer_topk_amd as moe
+    M, N, K = 70000, 32768, 384
+    al = moe.moe_align(torch.zeros(M, 1, dtype=torch.int32, device=dev), 1, 128)
+    g = torch.Generator(device=dev).manual_seed(11)
+    dc = torch.empty(M, N, dtype=BF, device=dev)
+    for i in range(0, M, 10000):
+        dc[i:i + 10000] = torch.randn(10000, N, generator=g, device=dev).to(BF)
+    a = torch.randn(M, K, generator=g, device=dev).to(BF)
+    for kind in (moe.MOE_GEMM_DOWN, moe.MOE_GEMM_GATE_UP):
+        dw = moe.moe_grouped_gemm_dw(kind, dc, a, al, M, 1, dtype=F32)
+        for c in (slice(0, 3), slice(16383, 16386), slice(N - 3, N)):
+            d, v = dc[:, c].double(), a.double()
+            want = d.t() @ v
+            close(dw[0, c], want.cpu(), (HALF[F32] * want.abs() + 2 * M * U * (d.abs().t() @ v.abs())).cpu(), "dw")

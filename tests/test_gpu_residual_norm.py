@@ -338,3 +338,43 @@ def test_long_rows_over_every_input(dev):
             args = [c[k].to(dev) for k in names]
             got = moe.moe_residual_norm_backward(*args, **kw, dh=args[over[0]], dy=args[over[1]])
             assert all(torch.equal(a, b) for a, b in zip(apart, got)), (H, over)
+
+
+def test_gradients_of_rows_past_four_gib(dev):
+    """Rows from both ends and the middle of 4.9 GB tensors, zeros elsewhere: the bits of a
+    row alone (a row's sums are its own), and column sums that add just those rows."""
+    import moe_layer_topk_amd as moe
+    M, H, at = 300000, 8192, [0, 149999, 299999]
+    c = make(3, H, BF, BF, True, True, "channel", True, 22)
+    kw = weights(c, dev)
+    big = {}
+    for name in ("h", "dh_out", "dx", "y"):
+        big[name] = torch.zeros(M, H, dtype=BF, device=dev)
+        big[name][at] = c[name].to(dev)
+    assert big["h"].numel() * 2 > 2 ** 32
+    alone = [moe.moe_residual_norm_backward(*(c[n][i:i + 1].to(dev) for n in ("h", "dh_out", "dx", "y")), **kw)
+             for i in range(3)]
+    dh, dy, *sums = moe.moe_residual_norm_backward(big["h"], big["dh_out"], big["dx"], big["y"], **kw, dh=big["dh_out"],
+                                                   dy=big["dx"])
+    for i, t in enumerate(at):
+        assert torch.equal(dh[t], alone[i][0][0]) and torch.equal(dy[t], alone[i][1][0]), t
+    for t in (1, 149998, 150000, M - 2):
+        assert not dh[t].any() and not dy[t].any()
+    for j, got in enumerate(sums):
+        parts = torch.stack([a[2 + j].double().cpu() for a in alone])
+        # (two float32 sums in any order; dpost and dgate are S times a weight on either side: 2 more)
+        close(got, parts.sum(0), 5 * U * parts.abs().sum(0), f"sum {j}")
+    # a gate a token: the form with conditions
+    kw["gate"] = torch.ones(M, 1, dtype=BF, device=dev)
+    g1 = torch.ones(1, 1, dtype=BF, device=dev)
+    alone = [moe.moe_residual_norm_backward(*(c[n][i:i + 1].to(dev) for n in ("h", "dh_out", "dx", "y")), **{**kw, "gate": g1})
+             for i in range(3)]
+    for name in ("dh_out", "dx"):
+        big[name].zero_()
+        big[name][at] = c[name].to(dev)
+    dh, dy, _, dgate, _ = moe.moe_residual_norm_backward(big["h"], big["dh_out"], big["dx"], big["y"], **kw, dh=big["dh_out"],
+                                                         dy=big["dx"])
+    for i, t in enumerate(at):
+        assert torch.equal(dh[t], alone[i][0][0]) and torch.equal(dy[t], alone[i][1][0]), t
+        assert torch.equal(dgate[t], alone[i][3][0])
+    assert int((dgate != 0).sum()) == 3
