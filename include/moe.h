@@ -501,8 +501,8 @@ moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const 
  * pair rows needs a pair_row of -1 at the other pairs, or zeros in their rows;
  * so do moe_unpermute, moe_combine and moe_unpermute_backward over y).
  * al, block_m (64 or 128): as
- * for moe_grouped_gemm.  Errors as there; one expert's weights of 4 GiB less
- * 64 KiB or more -> MOE_ERR_UNSUPPORTED. */
+ * for moe_grouped_gemm.  Errors as there; one expert's weights of more than
+ * 4 GiB less 64 KiB -> MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_gemm_dx(moe_gemm_kind kind, moe_dtype dtype, const void* dc, const void* w, const void* z,
                                const moe_align_bufs* al, int32_t M, int32_t topk, int32_t E, int32_t N, int32_t K,
                                int32_t block_m, void* da, void* act, void* stream);

@@ -185,7 +185,8 @@ moe_status moe_grouped_gemm_dx(moe_gemm_kind kind, moe_dtype dtype, const void* 
     moe_status st = check_grad(kind, dtype, M, topk, E, N, K, block_m);
     if (st != MOE_OK) return st;
     if (block_m != 64 && block_m != 128) return MOE_ERR_UNSUPPORTED;
-    // (32-bit offsets into an expert's weights, with room past the last row)
+    // (32-bit offsets into an expert's weights: a last column tile reads up to 256 bytes
+    // past the last row)
     if ((uint64_t)N * (uint64_t)K * 2 > 0xffff0000ull) return MOE_ERR_UNSUPPORTED;
     if ((kind == MOE_GEMM_GATE_UP && z) || (!z && act)) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;

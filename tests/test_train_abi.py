@@ -206,6 +206,20 @@ def test_dx(L, bal):
     assert f(da=ODD) == 5
 
 
+def test_dx_up_to_its_largest_expert(L, bal):
+    """4 GiB less 64 KiB of weights are taken (the next argument is looked at), one more
+    step of either size is not."""
+    def f(N, K):
+        return L.moe_grouped_gemm_dx(1, 1, NULL, FAKE, NULL, bal, 4, 2, 8, N, K, 64, FAKE, NULL, NULL)
+
+    assert 2 * 128 * 65535 * 256 == 2 ** 32 - 2 ** 16
+    assert f(128 * 65535, 256) == 1
+    assert f(256, 128 * 65535) == 1
+    assert f(128 * 131071, 128) == 3
+    assert f(128, 128 * 131071) == 3
+    assert f(128 * 65536, 256) == 3
+
+
 def test_dw(L, bal):
     def f(kind=1, dt=1, dc=FAKE, a=FAKE, al=bal, M=4, k=2, E=8, N=512, K=256, bm=64, odt=1, dw=FAKE):
         return L.moe_grouped_gemm_dw(kind, dt, dc, a, al, M, k, E, N, K, bm, odt, dw, NULL)
