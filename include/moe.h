@@ -481,6 +481,8 @@ size_t moe_residual_norm_workspace_size(int32_t M, int32_t H);
  *          is.  Sums over rows in float32, in a fixed order; with M = 0 the ones
  *          over rows become zeros.
  *  workspace  device, 256-byte aligned; its contents on entry do not matter.
+ *             Calls (and replays of captured ones) that overlap in time each
+ *             need their own.
  * dh and dy may each be one of the inputs; they differ from each other. */
 moe_status moe_residual_norm_backward(moe_dtype dtype, const void* h_out, const void* dh_out, const void* dx,
                                       const void* y, const moe_norm_spec* norm, int32_t M, int32_t H, void* dh, void* dy,

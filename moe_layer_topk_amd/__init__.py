@@ -605,7 +605,8 @@ def moe_residual_norm(h: torch.Tensor, y=None, post_weight=None, gate=None, scal
 def moe_residual_norm_backward(h_out: torch.Tensor, dh_out=None, dx=None, y=None, post_weight=None, gate=None,
                                scale: float = 1.0, pre_weight=None, eps: float = 1e-6, dh=None, dy=None, workspace=None):
     """Gradients of moe_residual_norm for dh_out (None: zero) and dx, from its h_out (h
-    where it had no y), y and weights.  dh and dy may be inputs.  Returns (dh, dy,
+    where it had no y), y and weights.  dh and dy may be inputs.  A workspace that is
+    given (uint8) is this call's alone until it has run.  Returns (dh, dy,
     dpost_weight, dgate, dpre_weight): rows in their own type, weights' in float32,
     None for what was not there."""
     dev = h_out.device

@@ -72,10 +72,12 @@ __device__ __forceinline__ unsigned tr_lane(int lane, int col0) {
 // weight rows are read 128 bytes at a time, whole lines, instead of 64 (128 experts of
 // 1536 x 2048, 16392 rows: 210 us against 233).
 //
-// What bounds them: at many rows an expert the power that products, transposing reads
-// and copies draw together (dx above: 0.87 PFLOP/s, matrix cores 50% busy at 1.4-1.5 GHz,
-// loads in flight 91% of the time; 740 us without copies and epilogue); at 128 rows the
-// way from L2 to LDS (8.7 TB/s); at 16 rows HBM (518 MB, 6.4 TB/s).
+// What bounds them: at many rows an expert the copies into LDS, 24 KB for the 2.1 MFLOP of
+// a stage (dx above: 11.3 GB at 10 TB/s, loads in flight 91% of the time; 1024 us without
+// the epilogue, 740 without the copies too), and with them the power that products,
+// transposing reads and copies draw together (0.87 PFLOP/s, matrix cores 50% busy at
+// 1.4-1.5 GHz; 16% faster on zeros); at 128 rows the same way from L2 to LDS (8.7 TB/s);
+// at 16 rows HBM (518 MB, 6.4 TB/s).
 enum DxMode { kDx, kDxSilu, kDxSiluNt, kZ };
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
@@ -158,7 +160,7 @@ grad_dx_kernel(GradCall g, int m_tiles, int o_tiles, int group) {
     for (int i = tid; i < BM; i += C::Threads) ids_s[i] = sorted[i];
 
     // sources of this wave's copies: rows of dc (kZ: of x), and of W 32 rows n (512 of
-    // their bytes; kZ: 256 rows, 64 bytes)
+    // their bytes; kZ: 256 rows, 128 bytes)
     const char* asrc[C::ALoads];
 #pragma unroll
     for (int j = 0; j < C::ALoads; ++j) {
@@ -506,7 +508,9 @@ __global__ void __launch_bounds__(SplitCfg::Threads) grad_dx_split_kernel(GradCa
 }
 
 // Up to 300 workgroups of it (of a guess: every expert hit, the last part of each half
-// full).  Regular against split, us, with its workgroups: dx of 8 experts, 2112 rows, 11008
+// full).  Regular against split, us, with its workgroups, on the same inputs again and
+// again (on inputs that change from call to call the first of them 168 and 83, the one of
+// 5888 terms 73 and 31, the one of 2560 terms 31 and 19): dx of 8 experts, 2112 rows, 11008
 // terms, 168: 147 and 64; 128 experts of 1536 x 2048, 8 rows, 128: 22 and 12; 4096 terms,
 // 288: 59 and 51; 1536 terms, 464: 29 and 32; through SiLU, 5888 terms, 39: 71 and 30;
 // 1024 terms, 576: 31 and 37; gate/up of 2560 terms, 32: 30 and 14; 2432 terms, 260: 34
@@ -695,7 +699,9 @@ grad_dw_kernel(GradCall g, int n_tiles, int k_tiles, int per_xcd) {
         for (int kt = nmain; kt < nst; ++kt) stage(kt, std::false_type{});
     }
 
-    // ---- epilogue: 32 n rows of the wave's tile at a time through LDS
+    // ---- epilogue: 32 n rows of the wave's tile at a time through LDS.  In float32 they
+    // reach past the ring into the row lists, which nothing reads any more: a workgroup
+    // has this one tile (one that went on to another would fetch wild rows).
     __syncthreads();
     constexpr int kElem = ODT == MOE_F32 ? 4 : 2, kRow = 32 * C::TN * kElem + 16;
     static_assert(C::Waves * 32 * kRow <= C::LdsBytes, "epilogue");

@@ -8,6 +8,7 @@
 // one direction is the other direction plus the dots, so two kernels serve four
 // calls.  Both go by tokens: a token's row is read (written) once, whatever topk,
 // and its topk expert rows once each, in 16-byte pieces a lane.  Bound by memory.
+// (moe_permute of up to 96 MB of rows goes by rows instead: permute_rows_kernel.)
 #include "moe_device.h"
 #include "moe_launch.h"
 #include "moe_train.h"
